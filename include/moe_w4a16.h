@@ -158,6 +158,48 @@ int moe_route_static(const void *x_dev, const void *w_router_dev, const float *b
                      int32_t *expert_offsets_dev, int32_t *sorted_pairs_dev, int32_t *pair_pos_dev,
                      int32_t *active_list_dev, int32_t *n_active_dev, void *stream);
 
+/* moe_route_scored: routing by scores over all experts, with the outputs of
+ * moe_route (same grouping, so the FFN calls and moe_combine take them).
+ *   logit[t][e] = RN32( exact sum_h x[t][h] * w_router[h][e] )
+ *   s[e] = softmax over all E logits, or 1 / (1 + exp(-logit[e]))
+ *   c[e] = s[e] + select_bias[e] (select_bias NULL: c = s): the choice value.  A
+ *     NaN choice value counts as -infinity; a bias of -infinity keeps an
+ *     expert last.
+ *   Groups (n_group > 1): experts are cut into n_group runs of E / n_group;
+ *     a group's value is its largest c (MOE_GROUP_MAX) or the sum of its two
+ *     largest (MOE_GROUP_TOP2; a NaN sum counts as -infinity); the topk_group
+ *     groups of largest value stay, ties to the lower group.
+ *   topk_ids[t][j]: the k largest c of the groups that stay, descending, ties
+ *     to the lower expert.
+ *   topk_w[t][j] = scale * s[topk_ids[t][j]], divided by the sum of the k chosen
+ *     scores if renormalize (0 where that sum is 0).  The bias is not in it.
+ * Scores, choice and group values are computed in fp64 and the weights rounded
+ * once to FP32: a selection does not depend on the batch it is in.  A token
+ * with a non-finite logit still gets k different experts (its weights may be
+ * NaN).
+ * logits_dev: FP32 [T][E] (no bias) or NULL.  Other outputs as for moe_route.
+ * rule: host pointer, read during the call.
+ * ws_dev / ws_bytes: moe_route_scored_workspace_size(T, H, E) bytes, 256-byte
+ *   aligned, ZERO-FILLED BEFORE ITS FIRST USE; every call leaves its counter
+ *   zero again (a workspace sized for T serves any T' <= T, with any rule); not
+ *   shared by calls that can overlap.
+ * Limits: as moe_route (T <= 65536, H <= 4096); x_dev 16-byte aligned;
+ *   k <= topk_group * (E / n_group); 0 < scale, finite. */
+enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum moe_group_score { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+typedef struct {
+    int score;                         /* MOE_SCORE_* */
+    int n_group, topk_group;           /* 1, 1: no groups */
+    int group_score;                   /* MOE_GROUP_* (unused when n_group = 1) */
+    int renormalize;                   /* nonzero: the k weights sum to scale */
+    float scale;                       /* factor of the weights */
+} moe_route_rule;
+size_t moe_route_scored_workspace_size(int T, int H, int E);
+int moe_route_scored(const void *x_dev, const void *w_router_dev, const float *select_bias_dev, int T, int H, int E,
+                     int k, const moe_route_rule *rule, float *logits_dev, int32_t *topk_ids_dev, float *topk_w_dev,
+                     int32_t *expert_offsets_dev, int32_t *sorted_pairs_dev, int32_t *pair_pos_dev,
+                     int32_t *active_list_dev, int32_t *n_active_dev, void *ws_dev, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------ expert FFN
  * Expert rows are addressed as rows_dev + slot_map_dev[e] * row_stride
  * (slot_map_dev NULL means slot e for expert e).  row_stride >=
@@ -530,6 +572,26 @@ int moe_fp16_expert_ffn(const void *x_dev, int T, int H, int I, int E, int k,
  * b): the residual connection that chains layers of a stack, x_{l+1} = x_l +
  * y_l (the sum of two FP16 values is exact in fp64 and rounded once). */
 int moe_residual_add(const void *a_dev, const void *b_dev, void *out_dev, long long n, void *stream);
+
+/* moe_residual_rmsnorm: the step from one layer to the next, T rows of H:
+ *   v = RN16(x + y) (y NULL: v = x)                     the residual stream
+ *   r = RN32( 1 / sqrt( sum_i v_i^2 / H + eps ) )       (fp64 sum and root)
+ *   n_i = RN32( RN32(v_i * r) * w_i )
+ *   sum = v (FP16);  norm = RN16(n) (FP16)
+ *   a = max(max_i |n_i|, 2^-100), q_scale = RN32(a / 448),
+ *   q_i = RN_e4m3( RN32( n_i * RN32(448 / a) ) )        n_i ~ q_i * q_scale
+ * Each step after the sum is one rounding of FP32, so the 8-bit codes do not
+ * depend on how the sum was ordered.  e4m3 is the finite format with largest
+ * value 448 (one byte a value).  A row that holds an infinity or a NaN gives
+ * NaN norms, codes and scale where IEEE arithmetic does.
+ * sum, norm and (q, q_scale [T]) may each be NULL, not all of them.  ld*: row
+ * strides in elements, >= H.  FP16 rows need 2-byte alignment only (rows of
+ * 16-byte multiples are fastest); q any.  sum and norm may each be x or y (the
+ * same pointer and stride), but not each other; otherwise outputs do not
+ * overlap inputs.  1 <= H <= 65536, T >= 0, 0 < eps <= 1.  w_dev: FP16 [H]. */
+int moe_residual_rmsnorm(const void *x_dev, long long ldx, const void *y_dev, long long ldy, const void *w_dev,
+                         float eps, int T, int H, void *sum_dev, long long lds, void *norm_dev, long long ldn,
+                         void *q_dev, long long ldq, float *q_scale_dev, void *stream);
 
 #ifdef __cplusplus
 }
