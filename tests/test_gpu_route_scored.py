@@ -1,0 +1,271 @@
+"""moe_route_scored against its definition in 64 bits on the host.
+
+Logits, selections and the grouping are compared bit for bit (the logits with
+the oracle's exact ones); the weights, one FP32 rounding of an fp64 value that
+differs from the host's by a few fp64 steps, within one FP32 step."""
+import numpy as np
+import pytest
+
+import oracle
+from w4a16_routed_expert_amd import synth
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+SOFTMAX, SIGMOID = 0, 1
+MAX, TOP2 = 0, 1
+
+
+def expected(logits, k, bias=None, score=SOFTMAX, n_group=1, topk_group=1, group=MAX, renorm=True, scale=1.0):
+    T, E = logits.shape
+    l = logits.astype(np.float64)
+    with np.errstate(invalid="ignore", over="ignore"):
+        if score == SOFTMAX:
+            e = np.exp(l - l.max(axis=1, keepdims=True))
+            s = e / e.sum(axis=1, keepdims=True)
+        else:
+            s = 1.0 / (1.0 + np.exp(-l))
+        c = s if bias is None else s + bias.astype(np.float64)
+    c = np.where(np.isnan(c), -np.inf, c)
+    allowed = np.ones((T, E), bool)
+    if n_group > 1:
+        gs = E // n_group
+        parts = np.sort(c.reshape(T, n_group, gs), axis=2)
+        with np.errstate(invalid="ignore"):
+            v = parts[:, :, -1] + (parts[:, :, -2] if group == TOP2 else 0.0)
+        v = np.where(np.isnan(v), -np.inf, v)
+        order = np.argsort(-v, axis=1, kind="stable")
+        kept = np.zeros((T, n_group), bool)
+        np.put_along_axis(kept, order[:, :topk_group], True, axis=1)
+        allowed = np.repeat(kept, gs, axis=1)
+    ids = np.empty((T, k), np.int32)
+    for t in range(T):                               # excluded experts after every allowed one
+        order = sorted(range(E), key=lambda e: (not allowed[t, e], -c[t, e], e))
+        ids[t] = order[:k]
+    w = np.take_along_axis(s, ids.astype(np.int64), axis=1)
+    if renorm:
+        den = w.sum(axis=1, keepdims=True)
+        w = np.where(den == 0.0, 0.0, w / np.where(den == 0.0, 1.0, den))
+    flat = ids.reshape(-1)
+    pairs = np.argsort(flat, kind="stable").astype(np.int32)
+    pos = np.empty_like(pairs)
+    pos[pairs] = np.arange(flat.size, dtype=np.int32)
+    counts = np.bincount(flat, minlength=E)
+    active = np.full(E, -1, np.int32)
+    live = np.flatnonzero(counts)
+    active[:live.size] = live
+    return dict(ids=ids, w=(w * float(np.float32(scale))).astype(np.float32), sorted_pairs=pairs, pair_pos=pos,
+                offsets=np.concatenate([[0], np.cumsum(counts)]).astype(np.int32), active=active,
+                n_active=np.array([live.size], np.int32))
+
+
+class Call:
+    """Buffers of one shape (with guards behind them) and the call on them."""
+
+    def __init__(self, T, H, E, k, ws=None):
+        from w4a16_routed_expert_amd import binding as B
+        self.B, self.dev = B, torch.device("cuda:0")
+        self.T, self.H, self.E, self.k = T, H, E, k
+        n = {"logits": (T * E, torch.float32), "ids": (T * k, torch.int32), "w": (T * k, torch.float32),
+             "offsets": (E + 1, torch.int32), "sorted_pairs": (T * k, torch.int32), "pair_pos": (T * k, torch.int32),
+             "active": (E, torch.int32), "n_active": (1, torch.int32)}
+        self.n = {name: v[0] for name, v in n.items()}
+        self.out = {name: torch.full((c + 64,), -77, dtype=dt, device=self.dev) for name, (c, dt) in n.items()}
+        need = B.moe_route_scored_workspace_size(T, H, E)
+        self.ws = torch.zeros(need, dtype=torch.uint8, device=self.dev) if ws is None else ws
+
+    def __call__(self, x, wr, bias, logits=True, stream=None, **rule):
+        B, o = self.B, self.out
+        r = B.route_rule(score=rule.get("score", SOFTMAX), n_group=rule.get("n_group", 1),
+                         topk_group=rule.get("topk_group", 1), group_score=rule.get("group", MAX),
+                         renormalize=rule.get("renorm", True), scale=rule.get("scale", 1.0))
+        B.moe_route_scored(x, wr, bias, self.T, self.H, self.E, self.k, r, o["logits"] if logits else None, o["ids"],
+                           o["w"], o["offsets"], o["sorted_pairs"], o["pair_pos"], o["active"], o["n_active"],
+                           self.ws, self.ws.numel(), stream)
+
+    def host(self):
+        torch.cuda.synchronize()
+        got = {}
+        for name, t in self.out.items():
+            assert bool((t[self.n[name]:] == -77).all()), f"{name}: written past its end"
+            got[name] = t[:self.n[name]].cpu().numpy()
+        got["ids"], got["w"] = got["ids"].reshape(self.T, self.k), got["w"].reshape(self.T, self.k)
+        got["logits"] = got["logits"].reshape(self.T, self.E)
+        assert int(self.ws[:256].sum()) == 0, "the counter is left nonzero"
+        return got
+
+
+def check(got, want, logits, what):
+    if logits is not None:
+        assert np.array_equal(got["logits"].view(np.uint32), logits.view(np.uint32)), f"{what}: logits differ"
+    for name in ("ids", "offsets", "sorted_pairs", "pair_pos", "active", "n_active"):
+        assert np.array_equal(got[name], want[name]), f"{what}: {name} differs"
+    g, w = got["w"].astype(np.float64), want["w"].astype(np.float64)
+    assert np.array_equal(np.isnan(g), np.isnan(w)), f"{what}: NaN weights"
+    m = ~np.isnan(w)
+    assert np.all(np.abs(g - w)[m] <= np.spacing(np.abs(want["w"]))[m].astype(np.float64)), f"{what}: weights"
+
+
+def device(*arrays):
+    return [None if a is None else torch.from_numpy(np.ascontiguousarray(a)).to("cuda:0") for a in arrays]
+
+
+def inputs(T, H, E, seed=0):
+    g = np.random.default_rng([seed, T, H, E])
+    x = g.standard_normal((T, H)).astype(np.float16)
+    wr = (g.standard_normal((H, E)) / np.sqrt(H) * 1.5).astype(np.float16)
+    return x, wr, (0.1 * g.standard_normal(E)).astype(np.float32)
+
+
+RULES = [dict(score=SOFTMAX, renorm=False), dict(score=SIGMOID, scale=2.5),
+         dict(score=SIGMOID, n_group=4, topk_group=2, group=TOP2, scale=2.5),
+         dict(score=SOFTMAX, n_group=4, topk_group=3, group=MAX)]
+
+
+@pytest.mark.parametrize("rule", RULES, ids=["softmax", "sigmoid", "sigmoid-groups", "softmax-groups"])
+@pytest.mark.parametrize("T,H,E,k", [(1, 128, 8, 2), (1, 2048, 64, 8), (5, 384, 12, 4), (32, 2048, 64, 8),
+                                     (64, 1408, 60, 4), (65, 256, 16, 3), (80, 128, 32, 8), (97, 640, 60, 4),
+                                     (129, 4096, 24, 5), (333, 2048, 64, 8), (1000, 256, 36, 6)])
+def test_equals_the_definition(T, H, E, k, rule):
+    x, wr, bias = inputs(T, H, E)
+    xd, wd, bd = device(x, wr, bias)
+    logits = oracle.router_logits(x, wr)
+    call = Call(T, H, E, k)
+    for b, b_dev in ((None, None), (bias, bd)):
+        for rep in range(2):                         # the workspace serves again
+            call(xd, wd, b_dev, logits=rep == 0, **rule)
+            check(call.host(), expected(logits, k, b, **rule), logits, f"T={T} E={E} bias={b is not None} rep={rep}")
+
+
+@pytest.mark.parametrize("T", [3, 200])
+@pytest.mark.parametrize("E,n_group,topk_group,k", [(1, 1, 1, 1), (2, 2, 1, 1), (63, 9, 4, 8), (64, 64, 8, 8),
+                                                    (64, 32, 4, 8), (33, 3, 1, 8), (64, 1, 1, 8), (7, 7, 7, 7)])
+def test_group_shapes(T, E, n_group, topk_group, k):
+    x, wr, bias = inputs(T, 256, E, 1)
+    xd, wd, bd = device(x, wr, bias)
+    logits = oracle.router_logits(x, wr)
+    call = Call(T, 256, E, k)
+    for group in (MAX, TOP2):
+        if group == TOP2 and E // n_group < 2:
+            continue
+        rule = dict(score=SIGMOID, n_group=n_group, topk_group=topk_group, group=group)
+        call(xd, wd, bd, **rule)
+        check(call.host(), expected(logits, k, bias, **rule), logits, f"E={E} groups={n_group}")
+
+
+@pytest.mark.parametrize("T", [4, 96])
+@pytest.mark.parametrize("rule", RULES, ids=["softmax", "sigmoid", "sigmoid-groups", "softmax-groups"])
+def test_ties_saturation_and_infinities(T, rule):
+    H, E, k = 256, 64, 8
+    g = np.random.default_rng(T)
+    # small whole numbers: many exactly equal logits; then equal columns, saturated and underflowed scores
+    x = g.integers(-1, 2, (T, H)).astype(np.float16)
+    wr = g.integers(-1, 2, (H, E)).astype(np.float16)
+    wr[:, 40:] = wr[:, 8:32]
+    x[0] = 0                                          # every logit 0
+    x[1] = 60000                                      # logits of millions: sigmoid 0 or 1, softmax one-hot
+    x[2] = -60000
+    bias = np.zeros(E, np.float32)
+    bias[3], bias[50], bias[20] = -np.inf, 0.5, -0.25
+    xd, wd, bd = device(x, wr, bias)
+    logits = oracle.router_logits(x, wr)
+    call = Call(T, H, E, k)
+    for b, b_dev in ((None, None), (bias, bd)):
+        call(xd, wd, b_dev, **rule)
+        check(call.host(), expected(logits, k, b, **rule), logits, f"T={T} bias={b is not None}")
+    # a bias that leaves fewer than k experts, or none, and a NaN bias
+    for left in (k - 2, 0):
+        b = np.full(E, -np.inf, np.float32)
+        b[5:5 + left] = 0
+        b[60] = np.nan
+        call(xd, wd, device(b)[0], **rule)
+        check(call.host(), expected(logits, k, b, **rule), logits, f"T={T}, {left} experts left")
+
+
+@pytest.mark.parametrize("T", [6, 70])
+def test_non_finite_tokens_leave_the_others_alone(T):
+    H, E, k = 256, 16, 4
+    x, wr, bias = inputs(T, H, E, 2)
+    clean = oracle.router_logits(x, wr)
+    x[1, 7], x[3, 0], x[T - 1, 5] = np.nan, np.inf, -np.inf
+    xd, wd, bd = device(x, wr, bias)
+    bad = [1, 3, T - 1]
+    good = [t for t in range(T) if t not in bad]
+    for rule in RULES:
+        call = Call(T, H, E, k)
+        call(xd, wd, bd, **rule)
+        got = call.host()
+        assert not np.isfinite(got["logits"][bad]).all(axis=1).any()
+        # the definition applied to the logits it returned
+        check(got, expected(got["logits"], k, bias, **rule), None, f"T={T}")
+        assert np.array_equal(got["logits"][good].view(np.uint32), clean[good].view(np.uint32))
+        assert all(len(set(row)) == k and min(row) >= 0 and max(row) < E for row in got["ids"].tolist())
+
+
+def test_logits_on_rounding_midpoints():
+    # exact logits that are FP32 ties (2^24 + 1 -> 2^24, 2^24 + 3 -> 2^24 + 4) in both kernels
+    H, E, k = 256, 8, 3
+    for T in (6, 100):
+        g = np.random.default_rng(17)
+        wr = (g.standard_normal((H, E)) * 1e-3).astype(np.float16)
+        x = (g.standard_normal((T, H)) * 1e-3).astype(np.float16)
+        wr[:4], x[:4], x[4:, :4] = 0, 0, 0
+        for t in range(4):
+            x[t, 0], x[t, 1] = 4096, 1
+        wr[0], wr[1] = 4096, np.array([1, 3, 2, 0, -1, -3, 5, 7], np.float16)
+        xd, wd = device(x, wr)
+        logits = oracle.router_logits(x, wr)
+        call = Call(T, H, E, k)
+        call(xd, wd, None, score=SIGMOID)
+        check(call.host(), expected(logits, k, score=SIGMOID), logits, f"T={T}")
+
+
+def test_unaligned_router_and_long_batch():
+    H, E, k, T = 128, 60, 8, 20000
+    x, wr, bias = inputs(T, H, E, 3)
+    xd, bd = device(x, bias)
+    flat = torch.zeros(H * E + 1, dtype=torch.float16, device="cuda:0")
+    wd = flat[1:].view(H, E)
+    wd.copy_(torch.from_numpy(wr))
+    logits = oracle.router_logits(x, wr)
+    rule = dict(score=SIGMOID, n_group=6, topk_group=3, group=TOP2)
+    call = Call(T, H, E, k)
+    call(xd, wd, bd, **rule)
+    check(call.host(), expected(logits, k, bias, **rule), logits, "router at an odd address")
+
+
+def test_selection_does_not_depend_on_the_batch():
+    cfg = synth.CONFIGS["olmoe"]
+    T = 256
+    x, wr = synth.make_x(cfg, T), synth.make_router(cfg)
+    xd, wd = device(x, wr)
+    rule = dict(score=SIGMOID, n_group=8, topk_group=4, group=TOP2)
+    whole = Call(T, cfg.H, cfg.E, cfg.k)
+    whole(xd, wd, None, **rule)
+    a = whole.host()
+    part = Call(40, cfg.H, cfg.E, cfg.k, ws=whole.ws)   # a workspace of a larger batch serves a smaller one
+    part(xd[100:140], wd, None, **rule)
+    b = part.host()
+    for name in ("logits", "ids", "w"):
+        assert np.array_equal(a[name][100:140], b[name]), name
+
+
+@pytest.mark.parametrize("T", [16, 160])
+def test_captured_replays(T):
+    H, E, k = 512, 64, 8
+    rule = dict(score=SIGMOID, n_group=8, topk_group=4, group=TOP2, scale=2.5)
+    x, wr, bias = inputs(T, H, E, 4)
+    xd, wd, bd = device(x, wr, bias)
+    call = Call(T, H, E, k)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        call(xd, wd, bd, **rule)
+        call(xd, wd, bd, **rule)                      # the second finds the counter at zero again
+    for step in range(3):
+        x2, _, _ = inputs(T, H, E, 10 + step)
+        xd.copy_(torch.from_numpy(x2))
+        graph.replay()
+        logits = oracle.router_logits(x2, wr)
+        check(call.host(), expected(logits, k, bias, **rule), logits, f"replay {step}")

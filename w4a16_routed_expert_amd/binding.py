@@ -35,10 +35,16 @@ MOE_FFN_PATH_GEMM = 2
 MOE_FFN_PATH_KSPLIT = 3
 MOE_FFN_PATH_ONE_LAUNCH = 4
 
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
+
 # Every symbol the header declares (checked by the CPU test suite).
 EXPORTS = (
     "moe_version", "moe_last_error", "moe_expert_row_bytes",
     "moe_route_workspace_size", "moe_route", "moe_route_exact", "moe_route_static_max_bytes", "moe_route_static",
+    "moe_route_scored_workspace_size", "moe_route_scored", "moe_residual_rmsnorm",
     "moe_w4a16_gateup", "moe_w4a16_down", "moe_w4a16_expert_ffn",
     "moe_combine", "moe_shared_ffn_workspace_size", "moe_shared_ffn", "moe_pack_fp16_tile8",
     "moe_layer_workspace_size", "moe_layer_forward", "moe_layer_forward_shared", "moe_residual_add",
@@ -55,6 +61,11 @@ class TableDesc(ctypes.Structure):
                 ("max_tokens", ctypes.c_int), ("host_source", ctypes.c_void_p),
                 ("host_row_stride", ctypes.c_size_t), ("initial_resident", ctypes.c_void_p),
                 ("row_digests", ctypes.c_void_p), ("slot_format", ctypes.c_int)]
+
+
+class RouteRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int),
+                ("group_score", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float)]
 
 
 class LayerBuffers(ctypes.Structure):
@@ -87,6 +98,7 @@ _lib = None
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 
 def load(path: str = LIB_PATH):
@@ -114,6 +126,14 @@ def load(path: str = LIB_PATH):
     L.moe_route_static_max_bytes.argtypes = []
     L.moe_route_static.restype = _i
     L.moe_route_static.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.moe_route_scored_workspace_size.restype = _sz
+    L.moe_route_scored_workspace_size.argtypes = [_i, _i, _i]
+    L.moe_route_scored.restype = _i
+    L.moe_route_scored.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, ctypes.POINTER(RouteRule), _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _vp, _vp, _sz, _vp]
+    L.moe_residual_rmsnorm.restype = _i
+    L.moe_residual_rmsnorm.argtypes = [_vp, _ll, _vp, _ll, _vp, ctypes.c_float, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll,
+                                       _vp, _vp]
     L.moe_w4a16_gateup.restype = _i
     L.moe_w4a16_gateup.argtypes = [_vp, _i, _i, _i, _i, _i, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp]
     L.moe_w4a16_down.restype = _i
@@ -244,6 +264,23 @@ def moe_route_static(x, w_router, bias, T, H, E, k, logits, topk_ids, topk_w, ex
                                    _p(active_list), _p(n_active), _s(stream)))
 
 
+def moe_route_scored_workspace_size(T: int, H: int, E: int) -> int:
+    return int(load().moe_route_scored_workspace_size(T, H, E))
+
+
+def route_rule(score=MOE_SCORE_SOFTMAX, n_group=1, topk_group=1, group_score=MOE_GROUP_MAX, renormalize=True,
+               scale=1.0) -> RouteRule:
+    return RouteRule(score, n_group, topk_group, group_score, 1 if renormalize else 0, scale)
+
+
+def moe_route_scored(x, w_router, select_bias, T, H, E, k, rule: RouteRule, logits, topk_ids, topk_w, expert_offsets,
+                     sorted_pairs, pair_pos, active_list, n_active, ws, ws_bytes, stream=None):
+    _check(load().moe_route_scored(_p(x), _p(w_router), _p(select_bias), T, H, E, k,
+                                   None if rule is None else ctypes.byref(rule), _p(logits), _p(topk_ids), _p(topk_w),
+                                   _p(expert_offsets), _p(sorted_pairs), _p(pair_pos), _p(active_list), _p(n_active),
+                                   _p(ws), ws_bytes, _s(stream)))
+
+
 def moe_w4a16_gateup(x, T, H, I, E, k, rows, row_stride, slot_map, expert_offsets, sorted_pairs, active_list,
                      n_active, h, status=None, mode=MOE_FFN_PATH_AUTO, stream=None):
     _check(load().moe_w4a16_gateup(_p(x), T, H, I, E, k, _p(rows), row_stride, _p(slot_map), _p(expert_offsets),
@@ -339,6 +376,25 @@ def moe_fp16_expert_ffn(x, T, H, I, E, k, rows, row_stride, slot_map, expert_off
 
 def moe_residual_add(a, b, out, n, stream=None):
     _check(load().moe_residual_add(_p(a), _p(b), _p(out), n, _s(stream)))
+
+
+def _ld(t, ld, width):
+    """Row stride in elements: `ld` if given, a 2-D tensor's own, else `width` (contiguous rows)."""
+    if ld is not None:
+        return ld
+    if t is None or isinstance(t, int) or t.dim() != 2:
+        return width
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("the values of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], width)
+
+
+def moe_residual_rmsnorm(x, y, w, eps, T, H, sum_out=None, norm=None, q=None, q_scale=None, ldx=None, ldy=None,
+                         ld_sum=None, ld_norm=None, ldq=None, stream=None):
+    """Row strides (elements) are those of 2-D tensors unless given."""
+    _check(load().moe_residual_rmsnorm(_p(x), _ld(x, ldx, H), _p(y), _ld(y, ldy, H), _p(w), eps, T, H, _p(sum_out),
+                                       _ld(sum_out, ld_sum, H), _p(norm), _ld(norm, ld_norm, H), _p(q),
+                                       _ld(q, ldq, H), _p(q_scale), _s(stream)))
 
 
 # ------------------------------------------------------------------ resident expert table

@@ -296,55 +296,20 @@ struct GroupLds {
     int ids[TOPK ? kGrpLdsIds : 1];
 };
 
-// Run by one block of NW wavefronts (DEV: the logits are read and the results
-// written at device scope, for blocks of the same launch).  With TOPK, first the top-k + softmax of
-// every token from the logits in a.lbuf (one wave per token, lane = expert);
-// then the stable counting sort of the T*k pairs by expert.  Wave w owns the
-// contiguous pair range [w*n/NW, (w+1)*n/NW): per-wave counts (LDS atomics),
-// a prefix over experts and waves gives each wave its starting position per
-// expert, then each wave walks its range 64 pairs at a time; a pair's rank
-// among equal experts of its chunk comes from a ballot.
-template <int NW, bool TOPK, bool DEV = false>
-__device__ void group_phase(const RouteArgs &a, GroupLds<NW, TOPK> &S)
+// The stable counting sort of the T*k pairs by expert, run by one block of NW
+// wavefronts (LDS_IDS: the ids are in S.ids, else in a.ids; DEV: the results
+// are written at device scope).  Wave w owns the contiguous pair range
+// [w*n/NW, (w+1)*n/NW): per-wave counts (LDS atomics), a prefix over experts
+// and waves gives each wave its starting position per expert, then each wave
+// walks its range 64 pairs at a time; a pair's rank among equal experts of its
+// chunk comes from a ballot.
+template <int NW, bool LDS_IDS, bool DEV>
+__device__ inline void group_sort(const RouteArgs &a, GroupLds<NW, LDS_IDS> &S)
 {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n = a.T * a.k, E = a.E;
-    if (TOPK) {
-        // A wave routes tokens wave, wave + NW, ...: the logit rows of kTopkChunk of
-        // them are requested together (one memory round trip per chunk, not one
-        // per pair of tokens), then routed kTopkBatch at a time.
-        for (int c0 = wave; c0 < a.T; c0 += NW * kTopkChunk) {
-            int tok[kTopkChunk];
-            float lv[kTopkChunk];
-#pragma unroll
-            for (int i = 0; i < kTopkChunk; ++i) {
-                tok[i] = c0 + i * NW;
-                // clamped (always valid) addresses: the loads issue back to back
-                const float *src = a.lbuf + (size_t)min(tok[i], a.T - 1) * E + min(lane, E - 1);
-                lv[i] = DEV ? moe::load_dev(src) : *src;
-            }
-            if (a.logits && a.logits != a.lbuf && lane < E) {
-#pragma unroll
-                for (int i = 0; i < kTopkChunk; ++i)
-                    if (tok[i] < a.T) a.logits[(size_t)tok[i] * E + lane] = lv[i];
-            }
-#pragma unroll
-            for (int i = 0; i < kTopkChunk; i += kTopkBatch) {
-                if (tok[i] >= a.T) break;                   // the rest of the chunk is past the batch
-                int tb[kTopkBatch];
-                float lb[kTopkBatch];
-#pragma unroll
-                for (int j = 0; j < kTopkBatch; ++j) {
-                    tb[j] = tok[i + j];
-                    lb[j] = lv[i + j];
-                }
-                topk_softmax_wave<kTopkBatch, DEV>(a, tb, lane, lb, S.ids);
-            }
-        }
-        __syncthreads();
-    }
     // ids of pair p: from LDS when this block just produced them, else from memory
-    auto id_of = [&](int p) { return TOPK ? S.ids[p] : a.ids[p]; };
+    auto id_of = [&](int p) { return LDS_IDS ? S.ids[p] : a.ids[p]; };
     const int p0 = (int)((long long)n * wave / NW), p1 = (int)((long long)n * (wave + 1) / NW);
     S.cnt[wave][lane] = 0;
     __syncthreads();
@@ -392,6 +357,52 @@ __device__ void group_phase(const RouteArgs &a, GroupLds<NW, TOPK> &S)
     }
 }
 
+// Run by one block of NW wavefronts (DEV: the logits are read and the results
+// written at device scope, for blocks of the same launch).  With TOPK, first the top-k + softmax of
+// every token from the logits in a.lbuf (one wave per token, lane = expert);
+// then the grouping.
+template <int NW, bool TOPK, bool DEV = false>
+__device__ void group_phase(const RouteArgs &a, GroupLds<NW, TOPK> &S)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int E = a.E;
+    if (TOPK) {
+        // A wave routes tokens wave, wave + NW, ...: the logit rows of kTopkChunk of
+        // them are requested together (one memory round trip per chunk, not one
+        // per pair of tokens), then routed kTopkBatch at a time.
+        for (int c0 = wave; c0 < a.T; c0 += NW * kTopkChunk) {
+            int tok[kTopkChunk];
+            float lv[kTopkChunk];
+#pragma unroll
+            for (int i = 0; i < kTopkChunk; ++i) {
+                tok[i] = c0 + i * NW;
+                // clamped (always valid) addresses: the loads issue back to back
+                const float *src = a.lbuf + (size_t)min(tok[i], a.T - 1) * E + min(lane, E - 1);
+                lv[i] = DEV ? moe::load_dev(src) : *src;
+            }
+            if (a.logits && a.logits != a.lbuf && lane < E) {
+#pragma unroll
+                for (int i = 0; i < kTopkChunk; ++i)
+                    if (tok[i] < a.T) a.logits[(size_t)tok[i] * E + lane] = lv[i];
+            }
+#pragma unroll
+            for (int i = 0; i < kTopkChunk; i += kTopkBatch) {
+                if (tok[i] >= a.T) break;                   // the rest of the chunk is past the batch
+                int tb[kTopkBatch];
+                float lb[kTopkBatch];
+#pragma unroll
+                for (int j = 0; j < kTopkBatch; ++j) {
+                    tb[j] = tok[i + j];
+                    lb[j] = lv[i + j];
+                }
+                topk_softmax_wave<kTopkBatch, DEV>(a, tb, lane, lb, S.ids);
+            }
+        }
+        __syncthreads();
+    }
+    group_sort<NW, TOPK, DEV>(a, S);
+}
+
 // Small batches: block = (token t, group g of kGroupE experts) computes those
 // logits (+ bias) into a.lbuf; route_group_kernel<true> then routes and
 // groups.  fp64 pass: lane = EQ*hp + eq, EQ = kGroupE/VEC lanes per
@@ -408,8 +419,9 @@ struct LogitsLds {
 };
 
 // DEV: the logits go to a.lbuf at device scope (read by another block of the
-// same launch).
-template <int VEC, bool DEV = false>
+// same launch).  NONFINITE: a sum that is infinite or NaN is the logit (the
+// integer path would read such inputs as numbers).
+template <int VEC, bool DEV = false, bool NONFINITE = false>
 __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
 {
     constexpr int EQ = kGroupE / VEC;
@@ -517,7 +529,8 @@ __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
         // most n roundings) is within a factor 1 + 2^-16 of the true sum|x*w|.
         // Hence err = 2^(ceil(log2 n) + 1 - 53) * B covers it.
         const double err = ldexp((double)B, kErrExp);
-        const bool certain = lane >= kGroupE || e >= E || (!a.force_exact && rn32_certain(v, err));
+        const bool certain = lane >= kGroupE || e >= E || (NONFINITE && !isfinite(v)) ||
+                             (!a.force_exact && rn32_certain(v, err));
         if (lane < kGroupE) s_logit[lane] = (float)v;
         const unsigned long long m = __ballot(!certain);
         if (lane == 0) s_redo = m;

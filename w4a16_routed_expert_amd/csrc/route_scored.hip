@@ -1,0 +1,508 @@
+// Routing by scores: router logits, softmax or sigmoid scores over all
+// experts, an optional balance bias and expert groups for the choice,
+// optionally renormalised weights, then moe_route's grouping.
+//
+//   l[e] = RN32(exact x . W[:, e])
+//   s[e] = exp(l[e] - max l) / sum exp(l - max l), or 1 / (1 + exp(-l[e]))
+//   c[e] = s[e] + bias[e]                         (a NaN counts as -inf)
+//   groups: expert e is in group e / (E / n_group); a group's value is its
+//     largest c or the sum of its two largest; the topk_group groups of
+//     largest value stay (ties to the lower group)
+//   ids = the k largest c of the groups that stay, descending, ties to the
+//     lower expert; w[j] = scale * s[ids[j]] (/ sum_j s[ids[j]])
+//
+// The logits are the correctly rounded FP32 values of route.hip, and scores,
+// choice values and group values are in fp64, so a selection does not depend
+// on summation order or batch size.
+//
+// Small batches: one launch as in the fused layer (a block per token and 16
+// experts; the block that finishes last selects and groups).  Larger ones:
+// route_tile_kernel computes 16 tokens x all experts per block with the fp64
+// matrix instruction and selects at once, then one launch places the pairs.
+#include "moe_internal.h"
+
+#include <climits>
+
+#include "route_dev.h"
+
+namespace {
+
+struct ScoreRule {
+    const float *bias;       // [E] or null: added to the score for the choice only
+    int softmax, n_group, topk_group, top2, renorm;
+    double scale;
+};
+
+// LDS of one wavefront's selection.
+struct SelectLds {
+    double c[64];
+};
+
+__device__ inline double lane_value(double v, int src)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, src);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), src);
+    return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+
+// How many of the first n lanes hold a larger value, or an equal one and a
+// lower lane (lanes of the mask `in` only).
+__device__ inline int rank_of(double v, int lane, int n, unsigned long long in)
+{
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!((in >> i) & 1ull)) continue;
+        const double o = lane_value(v, i);
+        rank += (o > v || (o == v && i < lane)) ? 1 : 0;
+    }
+    return rank;
+}
+
+// Scores, choice and weights of one token by one wavefront (lane = expert, lv
+// its logit).  Lane j < k ends with slot j's expert and weight.
+//
+// The k rounds compare the FP32 roundings of the choice values, which keep
+// their order except that different values may become equal: only when a
+// round's maximum is held by more than one lane are the fp64 values ranked.
+__device__ inline void select_wave(const ScoreRule &rule, int E, int k, int lane, float lv, SelectLds &S, int &id,
+                                   float &weight)
+{
+    const double l = (double)lv;
+    double s;
+    if (rule.softmax) {
+        const int top = wave_max(lane < E ? order_key(lv) : INT_MIN);
+        const float mx = __builtin_bit_cast(float, top ^ ((top >> 31) & 0x7FFFFFFF));
+        const double e = lane < E ? exp(l - (double)mx) : 0.0;
+        // one lane's sum for all: lanes add in different orders, and equal logits have equal scores
+        s = e / lane_value(sum_phases<1>(e), 0);
+    } else {
+        s = 1.0 / (1.0 + exp(-l));
+    }
+    double c = s;
+    if (rule.bias) c += (double)rule.bias[min(lane, E - 1)];
+    if (isnan(c)) c = -INFINITY;
+    unsigned long long in = E == 64 ? ~0ull : (1ull << E) - 1ull;
+    if (rule.n_group > 1) {
+        const int gs = E / rule.n_group;
+        S.c[lane] = c;
+        double best = -INFINITY, second = -INFINITY;
+        if (lane < rule.n_group) {
+            for (int i = 0; i < gs; ++i) {
+                const double v = S.c[lane * gs + i];
+                second = fmax(second, fmin(best, v));
+                best = fmax(best, v);
+            }
+        }
+        double value = rule.top2 ? best + second : best;
+        if (isnan(value)) value = -INFINITY;
+        const unsigned long long all = rule.n_group == 64 ? ~0ull : (1ull << rule.n_group) - 1ull;
+        const int rank = rank_of(value, lane, rule.n_group, all);
+        const unsigned long long kept = __ballot(lane < rule.n_group && rank < rule.topk_group);
+        in = __ballot(lane < E && ((kept >> (lane / gs)) & 1ull));
+    }
+    int key = ((in >> lane) & 1ull) ? order_key((float)c) : INT_MIN;
+    bool tie = false;
+    id = 0;
+    for (int j = 0; j < k; ++j) {
+        const int m = wave_max(key);
+        const unsigned long long who = __ballot(key == m);
+        const int win = (int)__builtin_ctzll(who);
+        tie = tie || (who & (who - 1ull));
+        if (lane == win) key = INT_MIN;
+        if (lane == j) id = win;
+    }
+    if (tie) {
+        const int rank = rank_of(c, lane, E, in);
+        for (int j = 0; j < k; ++j) {
+            const unsigned long long who = __ballot(((in >> lane) & 1ull) && rank == j);
+            if (lane == j) id = (int)__builtin_ctzll(who);
+        }
+    }
+    const uint64_t sb = __builtin_bit_cast(uint64_t, s);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * id, (int)(uint32_t)sb);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * id, (int)(uint32_t)(sb >> 32));
+    double w = __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+    if (rule.renorm) {
+        const double den = lane_value(sum_phases<1>(lane < k ? w : 0.0), 0);
+        w = den != 0.0 ? w / den : 0.0;        // every chosen score underflowed: weights 0
+    }
+    weight = (float)(w * rule.scale);
+}
+
+// ------------------------------------------------------------ small batches: one launch
+union SmallLds {
+    LogitsLds lg;
+    struct {
+        GroupLds<kSelWaves, true> gr;
+        SelectLds sel[kSelWaves];
+    } g;
+};
+
+template <int VEC>
+__global__ __launch_bounds__(kSelThreads) void route_scored_small_kernel(RouteArgs a, ScoreRule rule,
+                                                                         unsigned int *done)
+{
+    __shared__ SmallLds S;
+    __shared__ int s_last;
+    const int G = (a.E + kGroupE - 1) / kGroupE;
+    logits_block<VEC, true, true>(a, S.lg, blockIdx.x / G, blockIdx.x % G);
+    moe::wait_stores();                                     // this wave's logits are complete
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const unsigned int before = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = before == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int t = wave; t < a.T; t += kSelWaves) {
+        const float lv = moe::load_dev(a.lbuf + (size_t)t * a.E + min(lane, a.E - 1));
+        if (a.logits && lane < a.E) a.logits[(size_t)t * a.E + lane] = lv;
+        int id;
+        float w;
+        select_wave(rule, a.E, a.k, lane, lv, S.g.sel[wave], id, w);
+        if (lane < a.k) {
+            const size_t p = (size_t)t * a.k + lane;
+            a.ids[p] = id;
+            a.w[p] = w;
+            S.g.gr.ids[p] = id;
+        }
+    }
+    __syncthreads();
+    group_sort<kSelWaves, true, false>(a, S.g.gr);
+    if (threadIdx.x == 0) *done = 0u;
+}
+
+// ------------------------------------------------------------ larger batches
+// Block: 16 tokens x all experts.  Its 8 wavefronts split H; a wavefront's step
+// takes 32 values of H: lane 16q + j holds 8 of token j (values 8q .. 8q + 7 of
+// the step) and, per value, the NT experts NT*j .. NT*j + NT - 1 of that router
+// row, so one load of NT experts feeds NT matrix instructions (tile n's column
+// j is expert NT*j + n; the columns are a permutation of the experts).
+//   fp64 matrix instruction, 16x16x4: the products of FP16 values are exact in
+//   fp64; a wavefront's chain has H/8 additions per output and the 8 partial
+//   sums are added in order: at most H/8 + 8 additions on a path.
+constexpr int kTileT = 16;
+
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+template <int NT>
+struct TileLds {
+    double red[kSelWaves][kTileT][NT * 16];
+    float wsq[kSelWaves][NT * 16];
+    float xsq[kSelWaves][kTileT];
+    float logit[kTileT][64];
+    unsigned long long redo[kTileT];
+    long long ered[kSelWaves][2];
+    SelectLds sel[kSelWaves];
+    int cnt[MOE_MAX_EXPERTS];
+};
+
+template <int NT, bool WIDE>
+__global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, ScoreRule rule, int *counts)
+{
+    __shared__ TileLds<NT> S;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int E = a.E, H = a.H, T = a.T, k = a.k;
+    const int t0 = blockIdx.x * kTileT;
+    const int j = lane & 15, q = lane >> 4;
+    typedef WLoad<8> XL;
+    typedef WLoad<NT> L;
+
+    f64x4 acc[NT];
+    float wsq[NT], xsq = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        acc[n] = f64x4{0.0, 0.0, 0.0, 0.0};
+        wsq[n] = 0.0f;
+    }
+    const uint16_t *xrow = a.x + (size_t)min(t0 + j, T - 1) * H + 8 * q;
+    const int e0 = NT * j < E ? NT * j : 0;          // lanes past the experts repeat expert 0 (their columns are not read)
+    const uint16_t *wcol = a.wr + e0;
+    for (int h0 = 32 * wave; h0 < H; h0 += 32 * kSelWaves) {
+        const typename XL::T xv = XL::ld(xrow + h0);
+        uint16_t wv[8][NT];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint16_t *row = wcol + (size_t)(h0 + 8 * q + i) * E;
+            if constexpr (WIDE) {
+                const typename L::T v = L::ld(row);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) wv[i][n] = L::get(v, n);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) wv[i][n] = row[min(n, E - 1 - e0)];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float xf = (float)__builtin_bit_cast(_Float16, XL::get(xv, i));
+            xsq = fmaf(xf, xf, xsq);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float wf = (float)__builtin_bit_cast(_Float16, wv[i][n]);
+                wsq[n] = fmaf(wf, wf, wsq[n]);
+                acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)xf, (double)wf, acc[n], 0, 0, 0);
+            }
+        }
+    }
+    // partial sums of this wavefront: lane (q, j) holds tokens q + 4r of column j
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S.red[wave][q + 4 * r][NT * j + n] = acc[n][r];
+    xsq = sum_phases<16>(xsq);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) wsq[n] = sum_phases<16>(wsq[n]);
+    if (q == 0) {
+        S.xsq[wave][j] = xsq;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) S.wsq[wave][NT * j + n] = wsq[n];
+    }
+    if (tid < kTileT) S.redo[tid] = 0ull;
+    if (tid < MOE_MAX_EXPERTS) S.cnt[tid] = 0;
+    __syncthreads();
+    constexpr int PER = kTileT * NT * 16 / kSelThreads > 0 ? kTileT * NT * 16 / kSelThreads : 1;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int o = tid + i * kSelThreads;
+        const int tt = o / (NT * 16), e = o % (NT * 16);
+        if (tt >= kTileT || e >= E || t0 + tt >= T) continue;
+        double v = 0.0;
+        float X = 0.0f, W = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kSelWaves; ++w) {
+            v += S.red[w][tt][e];
+            X += S.xsq[w][tt];
+            W += S.wsq[w][e];
+        }
+        // |v - exact| <= n 2^-53 (1 + n 2^-53) sum|x w| for paths of at most n additions, and
+        // sum|x w| <= sqrt(X W) with both FP32 sums of exact squares (at most H roundings,
+        // H <= 4096) within a factor 1 + 2^-11 of their true values.
+        const double err = (double)(H / kSelWaves + kSelWaves + 1) * 0x1p-53 * sqrt((double)X * (double)W) *
+                           (1.0 + 0x1p-9);
+        S.logit[tt][e] = (float)v;
+        if (isfinite(v) && (a.force_exact || !rn32_certain(v, err))) atomicOr(&S.redo[tt], 1ull << e);
+    }
+    __syncthreads();
+    for (int tt = 0; tt < kTileT; ++tt) {
+        unsigned long long redo = S.redo[tt];
+        while (redo) {                               // rare: exact recomputation by the whole block
+            const int e = __builtin_ctzll(redo);
+            redo &= redo - 1ull;
+            const float l = exact_logit(a, reinterpret_cast<const _Float16 *>(a.x) + (size_t)(t0 + tt) * H, e, S.ered);
+            if (tid == 0) S.logit[tt][e] = l;
+        }
+    }
+    __syncthreads();
+    for (int tt = wave; tt < kTileT; tt += kSelWaves) {
+        const int t = t0 + tt;
+        if (t >= T) break;
+        const float lv = S.logit[tt][min(lane, E - 1)];
+        if (a.logits && lane < E) a.logits[(size_t)t * E + lane] = lv;
+        int id;
+        float w;
+        select_wave(rule, E, k, lane, lv, S.sel[wave], id, w);
+        if (lane < k) {
+            const size_t p = (size_t)t * k + lane;
+            a.ids[p] = id;
+            a.w[p] = w;
+            atomicAdd(&S.cnt[id], 1);
+        }
+    }
+    __syncthreads();
+    if (tid < E) counts[(size_t)blockIdx.x * E + tid] = S.cnt[tid];
+}
+
+// Places the pairs of `tiles` 16-token tiles per block: expert e's pairs of
+// tile g start at the expert's offset (all tiles' counts of the experts before
+// it) plus the counts of e in the tiles before g.
+constexpr int kPlaceWaves = 16;
+
+__global__ __launch_bounds__(kPlaceWaves * 64) void route_place_kernel(RouteArgs a, const int *counts, int G, int tiles)
+{
+    __shared__ int s_tot[kPlaceWaves][64], s_pre[kPlaceWaves][64], s_cnt[kPlaceWaves][64], s_base[kPlaceWaves][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int E = a.E, n = a.T * a.k, ec = min(lane, E - 1);
+    const int g0 = blockIdx.x * tiles;
+    int tot = 0, pre = 0;
+    constexpr int U = 8;
+    for (int g = wave; g < G; g += kPlaceWaves * U) {
+        int c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int gg = g + u * kPlaceWaves;
+            c[u] = gg < G ? counts[(size_t)gg * E + ec] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            tot += c[u];
+            pre += g + u * kPlaceWaves < g0 ? c[u] : 0;
+        }
+    }
+    // this block's pairs, each wavefront a contiguous range
+    const int b0 = g0 * kTileT * a.k, b1 = min(n, b0 + tiles * kTileT * a.k);
+    const int len = b1 - b0;
+    const int p0 = b0 + (int)((long long)len * wave / kPlaceWaves), p1 = b0 + (int)((long long)len * (wave + 1) / kPlaceWaves);
+    s_tot[wave][lane] = tot;
+    s_pre[wave][lane] = pre;
+    s_cnt[wave][lane] = 0;
+    for (int p = p0 + lane; p < p1; p += 64) atomicAdd(&s_cnt[wave][a.ids[p] & 63], 1);
+    __syncthreads();
+    if (wave == 0) {
+        int c = 0, before = 0;
+#pragma unroll
+        for (int w = 0; w < kPlaceWaves; ++w) {
+            c += s_tot[w][lane];
+            before += s_pre[w][lane];
+        }
+        if (lane >= E) c = 0;
+        const int incl = moe::wave_inclusive_sum(c), excl = incl - c;
+        int run = excl + before;
+        for (int w = 0; w < kPlaceWaves; ++w) {
+            s_base[w][lane] = run;
+            run += s_cnt[w][lane];
+        }
+        if (blockIdx.x == 0) {
+            const unsigned long long act = __ballot(lane < E && c > 0);
+            const int na = __popcll(act);
+            if (lane < E) {
+                a.offsets[lane] = excl;
+                if (c > 0) a.active[__popcll(act & ((1ull << lane) - 1ull))] = lane;
+                if (lane >= na) a.active[lane] = -1;
+                if (lane == E - 1) a.offsets[E] = incl;
+            }
+            if (lane == 0) a.n_active[0] = na;
+        }
+    }
+    __syncthreads();
+    const unsigned long long below = (1ull << lane) - 1ull;
+    for (int c0 = p0; c0 < p1; c0 += 64) {
+        const int p = c0 + lane;
+        const int e = p < p1 ? a.ids[p] & 63 : -1;
+        const unsigned long long peers = same_expert_lanes(e);
+        if (e >= 0) {
+            const int rank = __popcll(peers & below);
+            const int pos = s_base[wave][e] + rank;
+            a.sorted_pairs[pos] = p;
+            a.pair_pos[p] = pos;
+            if (rank == 0) s_base[wave][e] = pos + __popcll(peers);   // one leader per expert and chunk
+        }
+    }
+}
+
+constexpr int kScoredSmallT = 64;            // largest batch routed in one launch
+constexpr size_t kScoredCtrl = 256;          // the counter, before the logits or counts
+
+size_t scored_ws_bytes(int T, int E)
+{
+    const size_t lbuf = (size_t)(T < kScoredSmallT ? T : kScoredSmallT) * E * sizeof(float);
+    const size_t counts = (size_t)((T + kTileT - 1) / kTileT) * E * sizeof(int);
+    return kScoredCtrl + ((lbuf > counts ? lbuf : counts) + 255) / 256 * 256;
+}
+
+template <int NT>
+void launch_tiles(const RouteArgs &a, const ScoreRule &rule, int *counts, hipStream_t s)
+{
+    const dim3 grid((unsigned int)((a.T + kTileT - 1) / kTileT));
+    if (a.E % NT == 0 && moe::aligned(a.wr, 2 * NT))
+        hipLaunchKernelGGL((route_tile_kernel<NT, true>), grid, dim3(kSelThreads), 0, s, a, rule, counts);
+    else hipLaunchKernelGGL((route_tile_kernel<NT, false>), grid, dim3(kSelThreads), 0, s, a, rule, counts);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_route_scored_workspace_size(int T, int H, int E)
+{
+    (void)H;
+    if (T < 0 || T > 65536 || E < 1 || E > MOE_MAX_EXPERTS) return 0;
+    return scored_ws_bytes(T, E);
+}
+
+int moe_route_scored(const void *x_dev, const void *w_router_dev, const float *select_bias_dev, int T, int H, int E,
+                     int k, const moe_route_rule *rule, float *logits_dev, int32_t *topk_ids_dev, float *topk_w_dev,
+                     int32_t *expert_offsets_dev, int32_t *sorted_pairs_dev, int32_t *pair_pos_dev,
+                     int32_t *active_list_dev, int32_t *n_active_dev, void *ws_dev, size_t ws_bytes, void *stream)
+{
+    moe::clear_error();
+    const char *who = "moe_route_scored";
+    int rc = moe::check_shape(T, H, 0, E, k, false);
+    if (rc) return rc;
+    if (H > kMaxH) return moe::fail(MOE_ERR_UNSUPPORTED, "%s: H=%d > %d", who, H, kMaxH);
+    if (!rule) return moe::fail(MOE_ERR_INVALID_ARG, "%s: null rule", who);
+    if (rule->score != MOE_SCORE_SOFTMAX && rule->score != MOE_SCORE_SIGMOID)
+        return moe::fail(MOE_ERR_INVALID_ARG, "%s: unknown score %d", who, rule->score);
+    if (rule->group_score != MOE_GROUP_MAX && rule->group_score != MOE_GROUP_TOP2)
+        return moe::fail(MOE_ERR_INVALID_ARG, "%s: unknown group score %d", who, rule->group_score);
+    const int G = rule->n_group;
+    if (G < 1 || G > E || E % G)
+        return moe::fail(MOE_ERR_INVALID_ARG, "%s: n_group=%d must divide E=%d", who, G, E);
+    if (rule->topk_group < 1 || rule->topk_group > G)
+        return moe::fail(MOE_ERR_INVALID_ARG, "%s: topk_group=%d outside [1, n_group=%d]", who, rule->topk_group, G);
+    if (k > rule->topk_group * (E / G))
+        return moe::fail(MOE_ERR_INVALID_ARG, "%s: k=%d exceeds the %d experts of topk_group=%d groups", who, k,
+                         rule->topk_group * (E / G), rule->topk_group);
+    if (G > 1 && rule->group_score == MOE_GROUP_TOP2 && E / G < 2)
+        return moe::fail(MOE_ERR_INVALID_ARG, "%s: groups of one expert have no two largest", who);
+    if (!(rule->scale > 0.0f) || rule->scale > 3.0e38f)
+        return moe::fail(MOE_ERR_INVALID_ARG, "%s: scale=%g must be positive and finite", who, (double)rule->scale);
+    if (T == 0) return MOE_OK;
+    if (!x_dev || !w_router_dev || !topk_ids_dev || !topk_w_dev || !expert_offsets_dev || !sorted_pairs_dev ||
+        !pair_pos_dev || !active_list_dev || !n_active_dev)
+        return moe::fail(MOE_ERR_INVALID_ARG, "%s: null pointer argument", who);
+    if (!moe::aligned(x_dev, 16) || !moe::aligned(w_router_dev, 2))
+        return moe::fail(MOE_ERR_INVALID_ARG, "%s: x must be 16-byte and w_router 2-byte aligned", who);
+    if (!ws_dev || ws_bytes < scored_ws_bytes(T, E) || !moe::aligned(ws_dev, 256))
+        return moe::fail(MOE_ERR_WORKSPACE, "%s: the workspace needs %zu bytes, 256-byte aligned", who,
+                         scored_ws_bytes(T, E));
+
+    RouteArgs a;
+    a.x = (const uint16_t *)x_dev;
+    a.wr = (const uint16_t *)w_router_dev;
+    a.bias = nullptr;
+    a.T = T; a.H = H; a.E = E; a.k = k;
+    a.logits = logits_dev;
+    a.ids = topk_ids_dev;
+    a.w = topk_w_dev;
+    a.offsets = expert_offsets_dev;
+    a.sorted_pairs = sorted_pairs_dev;
+    a.pair_pos = pair_pos_dev;
+    a.active = active_list_dev;
+    a.n_active = n_active_dev;
+    a.force_exact = 0;
+    a.lbuf = (float *)((uint8_t *)ws_dev + kScoredCtrl);
+    ScoreRule r;
+    r.bias = select_bias_dev;
+    r.softmax = rule->score == MOE_SCORE_SOFTMAX;
+    r.n_group = G;
+    r.topk_group = rule->topk_group;
+    r.top2 = rule->group_score == MOE_GROUP_TOP2;
+    r.renorm = rule->renormalize != 0;
+    r.scale = (double)rule->scale;
+    hipStream_t s = (hipStream_t)stream;
+    if (T <= kScoredSmallT) {
+        unsigned int *done = (unsigned int *)ws_dev;
+        const unsigned int blocks = (unsigned int)T * (unsigned int)((E + kGroupE - 1) / kGroupE);
+        if (E % 2 == 0 && moe::aligned(w_router_dev, 4))
+            hipLaunchKernelGGL(route_scored_small_kernel<2>, dim3(blocks), dim3(kSelThreads), 0, s, a, r, done);
+        else hipLaunchKernelGGL(route_scored_small_kernel<1>, dim3(blocks), dim3(kSelThreads), 0, s, a, r, done);
+        return moe::check_launch(who);
+    }
+    int *counts = (int *)a.lbuf;
+    if (E <= 16) launch_tiles<1>(a, r, counts, s);
+    else if (E <= 32) launch_tiles<2>(a, r, counts, s);
+    else launch_tiles<4>(a, r, counts, s);
+    rc = moe::check_launch("moe_route_scored (select)");
+    if (rc) return rc;
+    const int tiles_total = (T + kTileT - 1) / kTileT;
+    // at least 4 tiles per block, and at most 256 blocks: every block reads all tiles' counts
+    const int tiles = tiles_total > 1024 ? (tiles_total + 255) / 256 : 4;
+    hipLaunchKernelGGL(route_place_kernel, dim3((unsigned int)((tiles_total + tiles - 1) / tiles)),
+                       dim3(kPlaceWaves * 64), 0, s, a, (const int *)counts, tiles_total, tiles);
+    return moe::check_launch("moe_route_scored (grouping)");
+}
+
+}  // extern "C"
