@@ -390,6 +390,30 @@ int moe_shared_ffn(const void *x_dev, const void *w_gate_dev, const void *w_up_d
                    const void *w_sgate_dev, int T, int H, int Is, float *shared_out_dev, float *shared_gate_dev,
                    void *ws_dev, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------ dense product
+ * moe_linear: the dense (non-routed) products of a stack, with their epilogue:
+ *   y[t][n] = RN16( act( s * sum_k x[t][k] W[n][k] + bias[n] ) + residual[t][n] )
+ * FP32 sums and epilogue, one rounding.  type:
+ *   MOE_LINEAR_FP16: x, W FP16, s = 1 (x_scale, w_scale NULL);
+ *   MOE_LINEAR_E4M3: x, W e4m3 bytes, s = x_scale[t] * w_scale[n] (FP32 [T], [N],
+ *     both required): takes moe_residual_rmsnorm's q and q_scale.
+ * act: MOE_ACT_NONE, MOE_ACT_SILU (v / (1 + exp(-v))), MOE_ACT_GELU (v Phi(v)) or
+ * MOE_ACT_GELU_TANH (its tanh form).  bias FP32 [N] and residual FP16 may be
+ * NULL.  x [T][K], W [N][K] row-major with row strides ldx, ldw; residual, y
+ * [T][N] with ldr, ldy (elements).  y may be residual (the same pointer and
+ * stride); otherwise y overlaps no input.
+ * Limits: 0 <= T <= 65536, 1 <= N <= 2^24, 16 <= K <= 2^20 and a multiple of 16,
+ *   ldx, ldw <= 2^22; rows of x and W start at multiples of 16 bytes; y and
+ *   residual rows need 2-byte alignment (8 is faster).
+ * ws_dev / ws_bytes: moe_linear_workspace_size(T, N, K, type) bytes, 256-byte
+ *   aligned, no initialization; not shared by calls that can overlap. */
+enum moe_linear_type { MOE_LINEAR_FP16 = 0, MOE_LINEAR_E4M3 = 1 };
+enum moe_activation { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3 };
+size_t moe_linear_workspace_size(int T, int N, int K, int type);
+int moe_linear(const void *x_dev, long long ldx, const float *x_scale_dev, const void *w_dev, long long ldw,
+               const float *w_scale_dev, const float *bias_dev, const void *residual_dev, long long ldr, int T, int N,
+               int K, int type, int act, void *y_dev, long long ldy, void *ws_dev, size_t ws_bytes, void *stream);
+
 /* ------------------------------------------------------------ resident expert table
  * Which experts have a published device row, and the miss path that brings a
  * missing row to the GPU ("Horizon RunMap - architecture", section

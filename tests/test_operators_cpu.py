@@ -84,3 +84,37 @@ def test_row_strides_of_tensors():
     assert B._ld(base, 77, 32) == 77 and B._ld(None, None, 5) == 5
     with pytest.raises(ValueError):
         B._ld(base.t(), None, 10)
+
+
+def linear(T=4, N=64, K=128, type=B.MOE_LINEAR_FP16, x=F, w=F, y=F, ws=F, ws_bytes=1 << 30, **kw):
+    B.moe_linear(x, w, T, N, K, type, y, ws=ws, ws_bytes=ws_bytes, stream=0, **kw)
+
+
+def test_linear_refusals():
+    E4M3 = B.MOE_LINEAR_E4M3
+    refused(lambda: linear(type=2), B.MOE_ERR_INVALID_ARG, "type")
+    refused(lambda: linear(act=4), B.MOE_ERR_INVALID_ARG, "activation")
+    refused(lambda: linear(act=-1), B.MOE_ERR_INVALID_ARG, "activation")
+    for kw in (dict(T=-1), dict(T=65537), dict(N=0), dict(N=(1 << 24) + 1), dict(K=0), dict(K=8), dict(K=24),
+               dict(K=(1 << 20) + 16)):
+        refused(lambda: linear(**kw), B.MOE_ERR_UNSUPPORTED, "=")
+    for kw in (dict(x=None), dict(w=None), dict(y=None)):
+        refused(lambda: linear(**kw), B.MOE_ERR_INVALID_ARG, "null")
+    for kw in (dict(x_scale=F), dict(w_scale=F), dict(x_scale=F, w_scale=F), dict(type=E4M3),
+               dict(type=E4M3, x_scale=F), dict(type=E4M3, w_scale=F)):
+        refused(lambda: linear(**kw), B.MOE_ERR_INVALID_ARG, "scale")
+    for kw in (dict(ldx=112), dict(ldw=112), dict(ldy=63), dict(residual=F, ldr=63)):
+        refused(lambda: linear(**kw), B.MOE_ERR_INVALID_ARG, "stride")
+    for kw in (dict(ldx=(1 << 22) + 16), dict(ldw=(1 << 22) + 16)):
+        refused(lambda: linear(**kw), B.MOE_ERR_UNSUPPORTED, "strides")
+    for kw in (dict(x=F + 8), dict(w=F + 8), dict(ldx=132), dict(ldw=132)):
+        refused(lambda: linear(**kw), B.MOE_ERR_INVALID_ARG, "16 bytes")
+    refused(lambda: linear(type=E4M3, x_scale=F, w_scale=F, ldx=136), B.MOE_ERR_INVALID_ARG, "16 bytes")
+    for kw in (dict(y=F + 1), dict(residual=F + 1), dict(bias=F + 2)):
+        refused(lambda: linear(**kw), B.MOE_ERR_INVALID_ARG, "aligned")
+    need = B.moe_linear_workspace_size(4, 64, 128, B.MOE_LINEAR_FP16)
+    for kw in (dict(ws=None), dict(ws_bytes=need - 1), dict(ws=F + 16)):
+        refused(lambda: linear(**kw), B.MOE_ERR_WORKSPACE, "workspace")
+    for args in ((-1, 8, 16, 0), (4, 0, 16, 0), (4, 8, 8, 0), (4, 8, 24, 1), (4, 8, 16, 2)):
+        assert B.moe_linear_workspace_size(*args) == 0
+    linear(T=0, x=None, w=None, y=None, ws=None, ws_bytes=0)    # nothing to do

@@ -40,11 +40,19 @@ MOE_SCORE_SIGMOID = 1
 MOE_GROUP_MAX = 0
 MOE_GROUP_TOP2 = 1
 
+MOE_LINEAR_FP16 = 0
+MOE_LINEAR_E4M3 = 1
+MOE_ACT_NONE = 0
+MOE_ACT_SILU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_GELU_TANH = 3
+
 # Every symbol the header declares (checked by the CPU test suite).
 EXPORTS = (
     "moe_version", "moe_last_error", "moe_expert_row_bytes",
     "moe_route_workspace_size", "moe_route", "moe_route_exact", "moe_route_static_max_bytes", "moe_route_static",
     "moe_route_scored_workspace_size", "moe_route_scored", "moe_residual_rmsnorm",
+    "moe_linear_workspace_size", "moe_linear",
     "moe_w4a16_gateup", "moe_w4a16_down", "moe_w4a16_expert_ffn",
     "moe_combine", "moe_shared_ffn_workspace_size", "moe_shared_ffn", "moe_pack_fp16_tile8",
     "moe_layer_workspace_size", "moe_layer_forward", "moe_layer_forward_shared", "moe_residual_add",
@@ -134,6 +142,10 @@ def load(path: str = LIB_PATH):
     L.moe_residual_rmsnorm.restype = _i
     L.moe_residual_rmsnorm.argtypes = [_vp, _ll, _vp, _ll, _vp, ctypes.c_float, _i, _i, _vp, _ll, _vp, _ll, _vp, _ll,
                                        _vp, _vp]
+    L.moe_linear_workspace_size.restype = _sz
+    L.moe_linear_workspace_size.argtypes = [_i, _i, _i, _i]
+    L.moe_linear.restype = _i
+    L.moe_linear.argtypes = [_vp, _ll, _vp, _vp, _ll, _vp, _vp, _vp, _ll, _i, _i, _i, _i, _i, _vp, _ll, _vp, _sz, _vp]
     L.moe_w4a16_gateup.restype = _i
     L.moe_w4a16_gateup.argtypes = [_vp, _i, _i, _i, _i, _i, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp]
     L.moe_w4a16_down.restype = _i
@@ -395,6 +407,18 @@ def moe_residual_rmsnorm(x, y, w, eps, T, H, sum_out=None, norm=None, q=None, q_
     _check(load().moe_residual_rmsnorm(_p(x), _ld(x, ldx, H), _p(y), _ld(y, ldy, H), _p(w), eps, T, H, _p(sum_out),
                                        _ld(sum_out, ld_sum, H), _p(norm), _ld(norm, ld_norm, H), _p(q),
                                        _ld(q, ldq, H), _p(q_scale), _s(stream)))
+
+
+def moe_linear_workspace_size(T: int, N: int, K: int, type: int) -> int:
+    return int(load().moe_linear_workspace_size(T, N, K, type))
+
+
+def moe_linear(x, w, T, N, K, type, y, x_scale=None, w_scale=None, bias=None, act=MOE_ACT_NONE, residual=None,
+               ws=None, ws_bytes=0, ldx=None, ldw=None, ldr=None, ldy=None, stream=None):
+    """Row strides (elements) are those of 2-D tensors unless given."""
+    _check(load().moe_linear(_p(x), _ld(x, ldx, K), _p(x_scale), _p(w), _ld(w, ldw, K), _p(w_scale), _p(bias),
+                             _p(residual), _ld(residual, ldr, N), T, N, K, type, act, _p(y), _ld(y, ldy, N), _p(ws),
+                             ws_bytes, _s(stream)))
 
 
 # ------------------------------------------------------------------ resident expert table
