@@ -15,7 +15,6 @@
 namespace {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
-typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -32,8 +31,11 @@ struct LinearArgs {
     long long ldy;
     int T, N, chunks;                    // chunks: 16-byte chunks of a row
     int act;
-    int quads;                           // y and residual rows are 8-byte aligned: four outputs at once
 };
+
+// Rows of y and of the residual may start at any element: 16-byte accesses
+// that assume element alignment only.
+struct __attribute__((packed, aligned(2))) Out8 { half8 v; };
 
 __device__ inline float activate(float v, int act)
 {
@@ -47,61 +49,93 @@ __device__ inline float activate(float v, int act)
     return v;
 }
 
-// Epilogue of outputs n .. n+3 of token t (those inside the matrix).
+// What the epilogue needs of outputs n .. n+7, read once per lane.
 template <bool E4M3>
-__device__ inline void finish4(const LinearArgs &a, int t, int n, f32x4 v)
-{
-    if (t >= a.T || n >= a.N) return;
-    const int m = min(4, a.N - n);
-    if constexpr (E4M3) {
-        const float sx = a.x_scale[t];
+struct Columns {
+    float scale[8], bias[8];
+    int n, m;                            // first output, and how many of the 8 are inside the matrix
+
+    __device__ inline void load(const LinearArgs &a, int first)
+    {
+        n = first;
+        m = min(8, a.N - n);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] *= sx * a.w_scale[n + min(r, m - 1)];
-    }
-    if (a.bias) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] += a.bias[n + min(r, m - 1)];
-    }
-    if (a.act != MOE_ACT_NONE) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = activate(v[r], a.act);
-    }
-    uint16_t *y = a.y + (long long)t * a.ldy + n;
-    const uint16_t *res = a.res ? a.res + (long long)t * a.ldr + n : nullptr;
-    if (m == 4 && a.quads) {
-        if (res) {
-            const half4 h = *reinterpret_cast<const half4 *>(res);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] += (float)h[r];
+        for (int r = 0; r < 8; ++r) {
+            const int c = min(n + r, a.N - 1);
+            scale[r] = E4M3 ? a.w_scale[c] : 1.0f;
+            bias[r] = a.bias ? a.bias[c] : 0.0f;
         }
-        half4 o;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = (_Float16)v[r];
-        *reinterpret_cast<half4 *>(y) = o;
-    } else {
+    }
+
+    // The 8 outputs of token t from their sums (lo, hi).
+    __device__ inline void finish(const LinearArgs &a, int t, f32x4 lo, f32x4 hi) const
+    {
+        if (t >= a.T || m <= 0) return;
+        float v[8];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if (r >= m) break;
-            float f = v[r];
-            if (res) f += (float)__builtin_bit_cast(_Float16, res[r]);
-            const _Float16 o = (_Float16)f;
-            y[r] = __builtin_bit_cast(uint16_t, o);
+            v[r] = lo[r];
+            v[4 + r] = hi[r];
+        }
+        if constexpr (E4M3) {
+            const float sx = a.x_scale[t];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] *= sx * scale[r];
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] += bias[r];
+        if (a.act != MOE_ACT_NONE) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] = activate(v[r], a.act);
+        }
+        uint16_t *y = a.y + (long long)t * a.ldy + n;
+        const uint16_t *res = a.res ? a.res + (long long)t * a.ldr + n : nullptr;
+        if (m == 8) {
+            if (res) {
+                const half8 h = reinterpret_cast<const Out8 *>(res)->v;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) v[r] += (float)h[r];
+            }
+            half8 o;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) o[r] = (_Float16)v[r];
+            reinterpret_cast<Out8 *>(y)->v = o;
+        } else {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                if (r >= m) break;
+                float f = v[r];
+                if (res) f += (float)__builtin_bit_cast(_Float16, res[r]);
+                const _Float16 o = (_Float16)f;
+                y[r] = __builtin_bit_cast(uint16_t, o);
+            }
         }
     }
-}
+};
 
 __device__ inline i32x8 join(i32x4 a, i32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
-// One 128-byte step along k of a 16 x 16 output: lane (g, r) = (lane / 16,
-// lane % 16) holds chunks g and g + 4 of its row of each operand (which k
-// they stand for is the same on both sides, and the order of the sum is free).
-template <bool E4M3>
-__device__ inline f32x4 mma(i32x4 w0, i32x4 w1, i32x4 x0, i32x4 x1, f32x4 c)
+__device__ inline half8 lo_half8(i32x8 v) { return __builtin_bit_cast(half8, __builtin_shufflevector(v, v, 0, 1, 2, 3)); }
+__device__ inline half8 hi_half8(i32x8 v) { return __builtin_bit_cast(half8, __builtin_shufflevector(v, v, 4, 5, 6, 7)); }
+
+// One 128-byte step along k of M 16 x 16 outputs that share their tokens:
+// lane (g, r) = (lane / 16, lane % 16) holds chunks g and g + 4 of its row of
+// each operand (which k they stand for is the same on both sides, and the
+// order of the sum is free).
+template <bool E4M3, int M>
+__device__ inline void mma(const i32x8 (&w)[M], i32x8 x, f32x4 (&c)[M])
 {
-    if constexpr (E4M3)
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w0, w1), join(x0, x1), c, 0, 0, 0, 0, 0, 0);
-    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, w0), __builtin_bit_cast(half8, x0), c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, w1), __builtin_bit_cast(half8, x1), c, 0, 0, 0);
+    if constexpr (E4M3) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) c[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[i], x, c[i], 0, 0, 0, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            c[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo_half8(w[i]), lo_half8(x), c[i], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            c[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi_half8(w[i]), hi_half8(x), c[i], 0, 0, 0);
+    }
 }
 
 __device__ inline __amdgpu_buffer_rsrc_t rows_rsrc(const uint8_t *base, long long ld, int rows, int chunks)
@@ -158,37 +192,62 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int f = 0; f < FT; ++f) acc[f] = mma<E4M3>(w[u][0], w[u][1], x[u][f][0], x[u][f][1], acc[f]);
+            for (int f = 0; f < FT; ++f) {
+                f32x4 c[1] = {acc[f]};
+                const i32x8 wu[1] = {join(w[u][0], w[u][1])};
+                mma<E4M3, 1>(wu, join(x[u][f][0], x[u][f][1]), c);
+                acc[f] = c[0];
+            }
     }
 #pragma unroll
     for (int f = 0; f < FT; ++f) s_acc[wave][f][lane] = acc[f];
     __syncthreads();
-    for (int f = wave; f < FT; f += NW) {
-        f32x4 v = s_acc[0][f][lane];
+    // two lanes a token: outputs 8h .. 8h + 7 are the results of lanes (2h, r) and (2h + 1, r)
+    if (tid < 32 * FT) {
+        const int t = tid >> 1, h = tid & 1;
+        const int f = t >> 4, at = 32 * h + (t & 15);
+        Columns<E4M3> cols;
+        cols.load(a, n0 + 8 * h);
+        f32x4 lo = s_acc[0][f][at], hi = s_acc[0][f][at + 16];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) v += s_acc[w][f][lane];
-        finish4<E4M3>(a, t0 + 16 * f + r, n0 + 4 * g, v);
+        for (int w = 1; w < NW; ++w) {
+            lo += s_acc[w][f][at];
+            hi += s_acc[w][f][at + 16];
+        }
+        cols.finish(a, t0 + t, lo, hi);
     }
 }
 
 // ------------------------------------------------------------ many tokens
-// Block tile BN outputs x BT tokens, WN x WT wavefronts, 128 bytes of k a
-// step, two steps in LDS: the loads of step k + 1 go straight to LDS while
-// step k is multiplied, one barrier a step.  A row of a step is 8 chunks;
-// chunk c of row r sits in slot c ^ (r & 7), so the 16 lanes that read one
-// chunk of 16 rows spread over all banks (the swizzle is in the addresses the
-// loads read from: a load's 64 lanes fill 1024 consecutive bytes of LDS).
-template <bool E4M3, int BN, int BT, int WN, int WT>
+// Block tile BN outputs x BT tokens by 4 wavefronts, 2 x 2, each BN/2 x BT/2 in
+// registers; 128 bytes of k a step.  A step's operands lie in LDS in three
+// parts: the tokens X, and the first and second half (WA, WB) of every
+// wavefront's output rows, each twice (steps k and k + 1).  Per step:
+//     barrier; ask for X, WA of step k + 2; read WB(k); multiply WA(k) . X(k)
+//     barrier; ask for WB of step k + 2; read X, WA of step k + 1; multiply WB(k) . X(k)
+// so a part is overwritten as soon as every wavefront holds it in registers,
+// each load from memory has a step and a half to arrive, and the reads of LDS
+// run under the matrix instructions: those of the next step's token tile j
+// replace tile j once it has met every row of WB.
+//   A row of a step is 8 chunks of 16 bytes; chunk c of row r sits in slot
+// c ^ (r & 7), so the 16 lanes that read one chunk of 16 rows spread over all
+// banks (a load's 64 lanes fill 1024 consecutive bytes of LDS: the swizzle is
+// in the addresses they read from).
+template <int OUTSTANDING>
+__device__ inline void arrive()
+{
+    // this wavefront's older loads have landed and its reads are in registers, then everyone's
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(OUTSTANDING) : "memory");
+}
+
+template <bool E4M3, int BN, int BT>
 __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t)
 {
-    constexpr int NW = WN * WT;
-    constexpr int FN = BN / WN / 16, FT = BT / WT / 16;
-    constexpr int GW = BN / 8 / NW, GX = BT / 8 / NW;      // loads of 8 rows per wavefront
-    static_assert(GW * 8 * NW == BN && GX * 8 * NW == BT, "whole loads");
-    // one array per step in LDS: the compiler then knows that the loads into
-    // one do not feed the reads of the other
-    __shared__ i32x4 s0[(BN + BT) * 8], s1[(BN + BT) * 8];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    constexpr int FN = BN / 32, FT = BT / 32, HN = FN / 2;       // 16 x 16 tiles of a wavefront; of a half of its rows
+    constexpr int LX = BT / 32, LW = BN / 64;                    // loads (8 rows) of X and of a half of W a wavefront
+    // separate arrays: the compiler then knows which loads a read of LDS depends on
+    __shared__ i32x4 sx0[BT * 8], sx1[BT * 8], sa0[BN * 4], sa1[BN * 4], sb0[BN * 4], sb1[BN * 4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, r = lane & 15;
 
     // blocks are dealt to the 8 XCDs in turn: give each a contiguous run of
@@ -206,79 +265,127 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 
     const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + n0 * a.ldw, a.ldw, min(BN, a.N - n0), a.chunks);
     const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + t0 * a.ldx, a.ldx, min(BT, a.T - t0), a.chunks);
-    const int lr = lane >> 3, lc = (lane & 7) ^ lr;        // row within a load, chunk of it
-    uint32_t off_w[GW], off_x[GX];
+    const int lr = lane >> 3, lc = (lane & 7) ^ lr;              // row within a load, chunk of it
+    uint32_t off_x[LX], off_a[LW], off_b[LW];
 #pragma unroll
-    for (int i = 0; i < GW; ++i) {
-        const int row = 8 * (i * NW + wave) + lr;
-        off_w[i] = n0 + row < a.N ? (uint32_t)(row * a.ldw) + 16u * lc : kOutside;
-    }
-#pragma unroll
-    for (int i = 0; i < GX; ++i) {
-        const int row = 8 * (i * NW + wave) + lr;
+    for (int i = 0; i < LX; ++i) {
+        const int row = 8 * (i * 4 + wave) + lr;
         off_x[i] = t0 + row < a.T ? (uint32_t)(row * a.ldx) + 16u * lc : kOutside;
     }
-    auto fetch = [&](i32x4 *s, int step) {
-        const bool in = 8 * step + lc < a.chunks;
 #pragma unroll
-        for (int i = 0; i < GW; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_void *)(s + (i * NW + wave) * 64), 16,
-                                                     in && off_w[i] != kOutside ? off_w[i] + 128u * step : kOutside, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < GX; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_void *)(s + BN * 8 + (i * NW + wave) * 64), 16,
-                                                     in && off_x[i] != kOutside ? off_x[i] + 128u * step : kOutside, 0, 0, 0);
+    for (int i = 0; i < LW; ++i) {
+        const int h = 8 * (i * 4 + wave) + lr, row = h / (BN / 4) * (BN / 2) + h % (BN / 4);
+        off_a[i] = n0 + row < a.N ? (uint32_t)(row * a.ldw) + 16u * lc : kOutside;
+        off_b[i] = n0 + row + BN / 4 < a.N ? (uint32_t)((row + BN / 4) * a.ldw) + 16u * lc : kOutside;
+    }
+    // load i of a part of step `step` (zeros past the last chunk)
+    auto fetch = [&](uint32_t off, const __amdgpu_buffer_rsrc_t &rsrc, i32x4 *s, int i, int step) {
+        const bool in = 8 * step + lc < a.chunks && off != kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(s + (i * 4 + wave) * 64), 16,
+                                                 in ? off + 128u * step : kOutside, 0, 0, 0);
     };
-    const int wn = wave / WT * (BN / WN), wt = wave % WT * (BT / WT);
-    f32x4 acc[FN][FT];
+    // loads [i0, i1) of X, then WA
+    auto fetch_xa = [&](i32x4 *x, i32x4 *pa, int i0, int i1, int step) {
 #pragma unroll
-    for (int i = 0; i < FN; ++i)
+        for (int i = i0; i < i1; ++i) {
+            if (i < LX) fetch(off_x[i], rx, x, i, step);
+            else fetch(off_a[i - LX], rw, pa, i - LX, step);
+        }
+    };
+    auto fetch_b = [&](i32x4 *pb, int i0, int i1, int step) {
 #pragma unroll
-        for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, pb, i, step);
+    };
     const int c0 = g ^ (r & 7), c1 = (g + 4) ^ (r & 7);
-    auto multiply = [&](const i32x4 *s) {
-        const i32x4 *pw = s + (wn + r) * 8, *px = s + (BN + wt + r) * 8;
-        i32x4 x[FT][2];
+    const int at_x = ((wave & 1) * (BT / 2) + r) * 8, at_w = ((wave >> 1) * (BN / 4) + r) * 8;
+    auto read = [&](const i32x4 *s, int at) { return join(s[at + c0], s[at + c1]); };
+    f32x4 acc[2][FT][HN];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+#pragma unroll
+            for (int i = 0; i < HN; ++i) acc[h][j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int steps = (a.chunks + 7) / 8;
+    i32x8 x[FT], wa[HN], wb[HN];
+    fetch_xa(sx0, sa0, 0, LX + LW, 0);
+    fetch_b(sb0, 0, LW, 0);
+    fetch_xa(sx1, sa1, 0, LX + LW, 1);
+    fetch_b(sb1, 0, LW, 1);
+    arrive<LX + 3 * LW>();
+#pragma unroll
+    for (int j = 0; j < FT; ++j) x[j] = read(sx0, at_x + j * 128);
+#pragma unroll
+    for (int i = 0; i < HN; ++i) wa[i] = read(sa0, at_w + i * 128);
+    // step k on parts (px, pa, pb), the next step's parts being ox and oa.
+    // The scheduling barriers keep each token tile's few loads and reads among
+    // its matrix instructions.
+    auto do_step = [&](int k, i32x4 *px, i32x4 *pa, i32x4 *pb, const i32x4 *ox, const i32x4 *oa) {
+        arrive<LX + 2 * LW>();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < FT; ++j) {
-            x[j][0] = px[j * 128 + c0];
-            x[j][1] = px[j * 128 + c1];
+            if (j < HN) wb[j] = read(pb, at_w + j * 128);
+            fetch_xa(px, pa, j * (LX + LW) / FT, (j + 1) * (LX + LW) / FT, k + 2);
+            mma<E4M3, HN>(wa, x[j], acc[0][j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
+        arrive<LX + 2 * LW>();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < FN; ++i) {
-            const i32x4 w0 = pw[i * 128 + c0], w1 = pw[i * 128 + c1];
-#pragma unroll
-            for (int j = 0; j < FT; ++j) acc[i][j] = mma<E4M3>(w0, w1, x[j][0], x[j][1], acc[i][j]);
+        for (int j = 0; j < FT; ++j) {
+            if (j < HN) wa[j] = read(oa, at_w + j * 128);
+            fetch_b(pb, j * LW / FT, (j + 1) * LW / FT, k + 2);
+            mma<E4M3, HN>(wb, x[j], acc[1][j]);
+            x[j] = read(ox, at_x + j * 128);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
-    const int steps = (a.chunks + 7) / 8;
-    auto arrive = [&]() {
-        __builtin_amdgcn_s_waitcnt(0x0F70);                // vmcnt(0): this wavefront's loads are in LDS
-        __syncthreads();
-    };
-    fetch(s0, 0);
-    for (int k = 0; k + 2 <= steps; k += 2) {
-        arrive();
-        fetch(s1, k + 1);
-        multiply(s0);
-        arrive();
-        fetch(s0, k + 2);                                  // past the end: zeros, never read
-        multiply(s1);
+    for (int k = 0; k < steps; k += 2) {                         // an odd last step is followed by one of zeros
+        do_step(k, sx0, sa0, sb0, sx1, sa1);
+        do_step(k + 1, sx1, sa1, sb1, sx0, sa0);
     }
-    if (steps & 1) {
-        arrive();
-        multiply(s0);
+    arrive<0>();                                                 // no load is on its way to LDS any more
+
+    // Epilogue: the sums pass through LDS, 2 x 16 tokens of a wavefront at a
+    // time, so that a lane finishes 8 neighbouring outputs of a token.
+    constexpr int CW = BN / 8;                                   // 4-output chunks of a wavefront's row
+    constexpr int PT = BT >= 64 ? 2 : 1;                         // token tiles at a time
+    static_assert(PT * 16 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
+    i32x4 *mine = ((wave & 2) ? sx1 : sx0) + (wave & 1) * (PT * 16 * CW);
+    constexpr int LPT = CW / 2;                                  // lanes a token
+    Columns<E4M3> cols;
+    const int lane_n = lane % LPT;
+    cols.load(a, n0 + (wave >> 1) * (BN / 2) + 8 * lane_n);
+    const int t_wave = t0 + (wave & 1) * (BT / 2);
+#pragma unroll 1
+    for (int p = 0; p < FT / PT; ++p) {
+#pragma unroll
+        for (int q = 0; q < FT / PT; ++q) {
+            if (q != p) continue;
+#pragma unroll
+            for (int u = 0; u < PT; ++u)
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+                    mine[(16 * u + r) * CW + ((4 * i + g) ^ (r & 7))] =
+                        __builtin_bit_cast(i32x4, acc[i / HN][q * PT + u][i % HN]);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll 1
+        for (int t = lane / LPT; t < 16 * PT; t += 64 / LPT) {
+            const f32x4 lo = __builtin_bit_cast(f32x4, mine[t * CW + ((2 * lane_n) ^ (t & 7))]);
+            const f32x4 hi = __builtin_bit_cast(f32x4, mine[t * CW + ((2 * lane_n + 1) ^ (t & 7))]);
+            cols.finish(a, t_wave + p * (16 * PT) + t, lo, hi);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FT; ++j) finish4<E4M3>(a, t0 + wt + 16 * j + r, n0 + wn + 16 * i + 4 * g, acc[i][j]);
 }
 
-template <bool E4M3, int BN, int BT, int WN, int WT>
-__global__ __launch_bounds__(WN * WT * 64) void linear_tile_kernel(LinearArgs a, int tiles_n, int tiles_t)
+template <bool E4M3, int BN, int BT>
+__global__ __launch_bounds__(256, BN + BT > 256 ? 1 : 2) void linear_tile_kernel(LinearArgs a, int tiles_n, int tiles_t)
 {
-    linear_tile<E4M3, BN, BT, WN, WT>(a, tiles_n, tiles_t);
+    linear_tile<E4M3, BN, BT>(a, tiles_n, tiles_t);
 }
 
 template <bool E4M3, int FT>
@@ -288,12 +395,11 @@ void launch_stream(const LinearArgs &a, hipStream_t s)
     hipLaunchKernelGGL((linear_stream_kernel<E4M3, FT, 8>), grid, dim3(512), 0, s, a);
 }
 
-template <bool E4M3, int BN, int BT, int WN, int WT>
+template <bool E4M3, int BN, int BT>
 void launch_tile(const LinearArgs &a, hipStream_t s)
 {
     const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT;
-    hipLaunchKernelGGL((linear_tile_kernel<E4M3, BN, BT, WN, WT>), dim3((unsigned int)(tn * tt)), dim3(WN * WT * 64), 0,
-                       s, a, tn, tt);
+    hipLaunchKernelGGL((linear_tile_kernel<E4M3, BN, BT>), dim3((unsigned int)(tn * tt)), dim3(256), 0, s, a, tn, tt);
 }
 
 template <bool E4M3>
@@ -304,9 +410,9 @@ void launch(const LinearArgs &a, hipStream_t s)
     if (a.T <= 64) return launch_stream<E4M3, 4>(a, s);
     const long long big = (long long)((a.N + 255) / 256) * ((a.T + 255) / 256);
     const long long mid = (long long)((a.N + 127) / 128) * ((a.T + 127) / 128);
-    if (big >= 200) return launch_tile<E4M3, 256, 256, 2, 4>(a, s);
-    if (mid >= 200) return launch_tile<E4M3, 128, 128, 2, 2>(a, s);
-    launch_tile<E4M3, 64, 64, 2, 2>(a, s);
+    if (big >= 200) return launch_tile<E4M3, 256, 256>(a, s);
+    if (mid >= 200) return launch_tile<E4M3, 128, 128>(a, s);
+    launch_tile<E4M3, 64, 64>(a, s);
 }
 
 constexpr int kMaxLd = 1 << 22;                  // elements: 256 rows stay within 32-bit offsets
@@ -371,7 +477,6 @@ int moe_linear(const void *x_dev, long long ldx, const float *x_scale_dev, const
     a.N = N;
     a.chunks = K * size / 16;
     a.act = act;
-    a.quads = moe::aligned(y_dev, 8) && ldy % 4 == 0 && (!residual_dev || (moe::aligned(residual_dev, 8) && ldr % 4 == 0));
     if (e4m3) launch<true>(a, (hipStream_t)stream);
     else launch<false>(a, (hipStream_t)stream);
     return moe::check_launch(who);
