@@ -37,16 +37,31 @@ struct LinearArgs {
 // that assume element alignment only.
 struct __attribute__((packed, aligned(2))) Out8 { half8 v; };
 
-__device__ inline float activate(float v, int act)
+// v / (1 + exp(-u)) with the hardware's reciprocal and exponential (each within
+// about a step of FP32, far below the output's FP16 rounding); exp overflows to
+// infinity for far negative u and the result is then 0.
+__device__ inline float gate(float v, float u)
 {
-    if (act == MOE_ACT_SILU) return v / (1.0f + __expf(-v));
-    if (act == MOE_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    if (act == MOE_ACT_GELU_TANH) {
-        // 0.5 v (1 + tanh u) = v / (1 + exp(-2u))
-        const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
-        return v / (1.0f + __expf(-2.0f * u));
-    }
-    return v;
+    return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u * -1.44269504f));
+}
+
+// v Phi(v) = max(v, 0) - |v|/2 erfc(|v| / sqrt 2).  erfc(z) = exp(-z^2) P(t),
+// t = 1 / (1 + 0.37 z), P of degree 7 without a constant term: a weighted
+// least-squares fit of exp(z^2) erfc(z), made equal-rippled by reweighting;
+// relative error 1.7e-6 in FP32 over z <= 12 (past it the product is 0 in FP16).
+__device__ inline float gelu(float v)
+{
+    const float u = fminf(fabsf(v), 64.0f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(u, 0.26162952f, 1.0f));
+    float p = -0.138180092f;
+    p = fmaf(p, t, 0.419946969f);
+    p = fmaf(p, t, -0.163837433f);
+    p = fmaf(p, t, 0.300842702f);
+    p = fmaf(p, t, 0.159155518f);
+    p = fmaf(p, t, 0.21359317f);
+    p = fmaf(p, t, 0.208480641f);
+    const float tail = 0.5f * u * t * p * __builtin_amdgcn_exp2f(u * u * -0.72134752f);
+    return (v < 0.0f ? 0.0f : v) - tail;         // a NaN stays one
 }
 
 // What the epilogue needs of outputs n .. n+7, read once per lane.
@@ -67,47 +82,55 @@ struct Columns {
         }
     }
 
-    // The 8 outputs of token t from their sums (lo, hi).
-    __device__ inline void finish(const LinearArgs &a, int t, f32x4 lo, f32x4 hi) const
+    __device__ inline half8 residual(const LinearArgs &a, int t) const
     {
-        if (t >= a.T || m <= 0) return;
+        half8 h = {};
+        if (!a.res || t >= a.T || m <= 0) return h;
+        const uint16_t *res = a.res + (long long)t * a.ldr + n;
+        if (m == 8) return reinterpret_cast<const Out8 *>(res)->v;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            const _Float16 f = __builtin_bit_cast(_Float16, res[min(r, m - 1)]);
+            h[r] = f;
+        }
+        return h;
+    }
+
+    // The 8 outputs of token t from their sums (lo, hi), the token's scale and
+    // residuals.
+    __device__ inline void finish(const LinearArgs &a, int t, f32x4 lo, f32x4 hi, float sx, half8 res) const
+    {
         float v[8];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             v[r] = lo[r];
             v[4 + r] = hi[r];
         }
-        if constexpr (E4M3) {
-            const float sx = a.x_scale[t];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) v[r] *= sx * scale[r];
+        for (int r = 0; r < 8; ++r) v[r] = E4M3 ? fmaf(v[r], sx * scale[r], bias[r]) : v[r] + bias[r];
+        if (a.act == MOE_ACT_SILU) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] = gate(v[r], v[r]);
+        } else if (a.act == MOE_ACT_GELU) {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] = gelu(v[r]);
+        } else if (a.act == MOE_ACT_GELU_TANH) {
+            // 0.5 v (1 + tanh u) = v / (1 + exp(-2u)), u = sqrt(2/pi) (v + 0.044715 v^3)
+#pragma unroll
+            for (int r = 0; r < 8; ++r) v[r] = gate(v[r], v[r] * fmaf(0.07135481627f * v[r], v[r], 1.5957691216f));
         }
+        half8 o;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] += bias[r];
-        if (a.act != MOE_ACT_NONE) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) v[r] = activate(v[r], a.act);
-        }
+        for (int r = 0; r < 8; ++r) o[r] = (_Float16)(v[r] + (float)res[r]);
+        if (t >= a.T || m <= 0) return;
         uint16_t *y = a.y + (long long)t * a.ldy + n;
-        const uint16_t *res = a.res ? a.res + (long long)t * a.ldr + n : nullptr;
         if (m == 8) {
-            if (res) {
-                const half8 h = reinterpret_cast<const Out8 *>(res)->v;
-#pragma unroll
-                for (int r = 0; r < 8; ++r) v[r] += (float)h[r];
-            }
-            half8 o;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) o[r] = (_Float16)v[r];
             reinterpret_cast<Out8 *>(y)->v = o;
         } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                if (r >= m) break;
-                float f = v[r];
-                if (res) f += (float)__builtin_bit_cast(_Float16, res[r]);
-                const _Float16 o = (_Float16)f;
-                y[r] = __builtin_bit_cast(uint16_t, o);
+                const _Float16 h = o[r];
+                if (r < m) y[r] = __builtin_bit_cast(uint16_t, h);
             }
         }
     }
@@ -214,7 +237,8 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
             lo += s_acc[w][f][at];
             hi += s_acc[w][f][at + 16];
         }
-        cols.finish(a, t0 + t, lo, hi);
+        const half8 res = cols.residual(a, t0 + t);
+        cols.finish(a, t0 + t, lo, hi, E4M3 ? a.x_scale[min(t0 + t, a.T - 1)] : 1.0f, res);
     }
 }
 
@@ -247,6 +271,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     constexpr int LX = BT / 32, LW = BN / 64;                    // loads (8 rows) of X and of a half of W a wavefront
     // separate arrays: the compiler then knows which loads a read of LDS depends on
     __shared__ i32x4 sx0[BT * 8], sx1[BT * 8], sa0[BN * 4], sa1[BN * 4], sb0[BN * 4], sb1[BN * 4];
+    __shared__ float s_scale[E4M3 ? BT : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, r = lane & 15;
 
@@ -263,6 +288,9 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     const int in_run = tile % run;
     const int t0 = (first + in_run % height) * BT, n0 = in_run / height * BN;
 
+    if constexpr (E4M3) {
+        if ((int)threadIdx.x < BT) s_scale[threadIdx.x] = a.x_scale[min(t0 + (int)threadIdx.x, a.T - 1)];
+    }
     const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + n0 * a.ldw, a.ldw, min(BN, a.N - n0), a.chunks);
     const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + t0 * a.ldx, a.ldx, min(BT, a.T - t0), a.chunks);
     const int lr = lane >> 3, lc = (lane & 7) ^ lr;              // row within a load, chunk of it
@@ -354,11 +382,11 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     constexpr int PT = BT >= 64 ? 2 : 1;                         // token tiles at a time
     static_assert(PT * 16 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
     i32x4 *mine = ((wave & 2) ? sx1 : sx0) + (wave & 1) * (PT * 16 * CW);
-    constexpr int LPT = CW / 2;                                  // lanes a token
+    constexpr int LPT = CW / 2, TPI = 64 / LPT;                  // lanes a token, tokens at once
     Columns<E4M3> cols;
     const int lane_n = lane % LPT;
     cols.load(a, n0 + (wave >> 1) * (BN / 2) + 8 * lane_n);
-    const int t_wave = t0 + (wave & 1) * (BT / 2);
+    const int t_wave = (wave & 1) * (BT / 2);
 #pragma unroll 1
     for (int p = 0; p < FT / PT; ++p) {
 #pragma unroll
@@ -372,11 +400,22 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
                         __builtin_bit_cast(i32x4, acc[i / HN][q * PT + u][i % HN]);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        // the next token's sums and residuals are asked for before this one's are finished
+        int t = lane / LPT;
+        const int t_first = t_wave + p * (16 * PT);
+        half8 res = cols.residual(a, t0 + t_first + t);
+        i32x4 lo = mine[t * CW + ((2 * lane_n) ^ (t & 7))], hi = mine[t * CW + ((2 * lane_n + 1) ^ (t & 7))];
 #pragma unroll 1
-        for (int t = lane / LPT; t < 16 * PT; t += 64 / LPT) {
-            const f32x4 lo = __builtin_bit_cast(f32x4, mine[t * CW + ((2 * lane_n) ^ (t & 7))]);
-            const f32x4 hi = __builtin_bit_cast(f32x4, mine[t * CW + ((2 * lane_n + 1) ^ (t & 7))]);
-            cols.finish(a, t_wave + p * (16 * PT) + t, lo, hi);
+        for (; t < 16 * PT; t += TPI) {
+            const int tn = min(t + TPI, 16 * PT - 1);
+            const half8 res_next = cols.residual(a, t0 + t_first + tn);
+            const i32x4 lo_next = mine[tn * CW + ((2 * lane_n) ^ (tn & 7))];
+            const i32x4 hi_next = mine[tn * CW + ((2 * lane_n + 1) ^ (tn & 7))];
+            cols.finish(a, t0 + t_first + t, __builtin_bit_cast(f32x4, lo), __builtin_bit_cast(f32x4, hi),
+                        E4M3 ? s_scale[t_first + t] : 1.0f, res);
+            res = res_next;
+            lo = lo_next;
+            hi = hi_next;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
