@@ -16,6 +16,7 @@ namespace {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
@@ -138,28 +139,48 @@ struct Columns {
 
 __device__ inline i32x8 join(i32x4 a, i32x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
-__device__ inline half8 lo_half8(i32x8 v) { return __builtin_bit_cast(half8, __builtin_shufflevector(v, v, 0, 1, 2, 3)); }
-__device__ inline half8 hi_half8(i32x8 v) { return __builtin_bit_cast(half8, __builtin_shufflevector(v, v, 4, 5, 6, 7)); }
-
-// One 128-byte step along k of M 16 x 16 outputs that share their tokens:
-// lane (g, r) = (lane / 16, lane % 16) holds chunks g and g + 4 of its row of
-// each operand (which k they stand for is the same on both sides, and the
-// order of the sum is free).
-template <bool E4M3, int M>
-__device__ inline void mma(const i32x8 (&w)[M], i32x8 x, f32x4 (&c)[M])
-{
-    if constexpr (E4M3) {
-#pragma unroll
-        for (int i = 0; i < M; ++i) c[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[i], x, c[i], 0, 0, 0, 0, 0, 0);
-    } else {
-#pragma unroll
-        for (int i = 0; i < M; ++i)
-            c[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo_half8(w[i]), lo_half8(x), c[i], 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < M; ++i)
-            c[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi_half8(w[i]), hi_half8(x), c[i], 0, 0, 0);
+// One 128-byte step along k of an MT x MT output: lane (g, r) = (lane / MT,
+// lane % MT) reads its row r's chunks, kParts matrix instructions long (which
+// k a chunk stands for is the same for both operands, and the order of the sum
+// is free).  Its results 4b .. 4b + 3 are outputs n = 8b (32) + 4g .. + 3 of
+// token r.
+template <bool E4M3, int MT>
+struct Step;
+template <>
+struct Step<true, 16> {
+    static constexpr int kParts = 1;
+    typedef i32x8 Operand;
+    typedef f32x4 Acc;
+    static __device__ inline Operand pick(const i32x4 (&c)[2], int) { return join(c[0], c[1]); }
+    static __device__ inline Operand read(const i32x4 *row, int g, int swz, int) { return join(row[g ^ swz], row[(g + 4) ^ swz]); }
+    static __device__ inline Acc mma(Operand w, Operand x, Acc c)
+    {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, 0, 0, 0);
     }
-}
+};
+template <>
+struct Step<false, 16> {
+    static constexpr int kParts = 2;
+    typedef i32x4 Operand;
+    typedef f32x4 Acc;
+    static __device__ inline Operand pick(const i32x4 (&c)[2], int part) { return c[part]; }
+    static __device__ inline Operand read(const i32x4 *row, int g, int swz, int part) { return row[(g + 4 * part) ^ swz]; }
+    static __device__ inline Acc mma(Operand w, Operand x, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, w), __builtin_bit_cast(half8, x), c, 0, 0, 0);
+    }
+};
+template <>
+struct Step<false, 32> {
+    static constexpr int kParts = 4;
+    typedef i32x4 Operand;
+    typedef f32x16 Acc;
+    static __device__ inline Operand read(const i32x4 *row, int g, int swz, int part) { return row[(g + 2 * part) ^ swz]; }
+    static __device__ inline Acc mma(Operand w, Operand x, Acc c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8, w), __builtin_bit_cast(half8, x), c, 0, 0, 0);
+    }
+};
 
 __device__ inline __amdgpu_buffer_rsrc_t rows_rsrc(const uint8_t *base, long long ld, int rows, int chunks)
 {
@@ -177,6 +198,7 @@ constexpr uint32_t kOutside = 0xFFFFFF00u;       // an offset past every buffer:
 template <bool E4M3, int FT, int NW>
 __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 {
+    typedef Step<E4M3, 16> S;
     constexpr int U = FT >= 4 ? 2 : 4;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int g = lane >> 4, r = lane & 15;
@@ -215,12 +237,10 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int f = 0; f < FT; ++f) {
-                f32x4 c[1] = {acc[f]};
-                const i32x8 wu[1] = {join(w[u][0], w[u][1])};
-                mma<E4M3, 1>(wu, join(x[u][f][0], x[u][f][1]), c);
-                acc[f] = c[0];
-            }
+            for (int f = 0; f < FT; ++f)
+#pragma unroll
+                for (int h = 0; h < S::kParts; ++h)
+                    acc[f] = S::mma(S::pick(w[u], h), S::pick(x[u][f], h), acc[f]);
     }
 #pragma unroll
     for (int f = 0; f < FT; ++f) s_acc[wave][f][lane] = acc[f];
@@ -254,7 +274,7 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 // run under the matrix instructions: those of the next step's token tile j
 // replace tile j once it has met every row of WB.
 //   A row of a step is 8 chunks of 16 bytes; chunk c of row r sits in slot
-// c ^ (r & 7), so the 16 lanes that read one chunk of 16 rows spread over all
+// c ^ (r / 2 & 7), so the lanes that read one chunk of many rows spread over all
 // banks (a load's 64 lanes fill 1024 consecutive bytes of LDS: the swizzle is
 // in the addresses they read from).
 template <int OUTSTANDING>
@@ -264,16 +284,18 @@ __device__ inline void arrive()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(OUTSTANDING) : "memory");
 }
 
-template <bool E4M3, int BN, int BT>
+template <bool E4M3, int BN, int BT, int MT>
 __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t)
 {
-    constexpr int FN = BN / 32, FT = BT / 32, HN = FN / 2;       // 16 x 16 tiles of a wavefront; of a half of its rows
+    typedef Step<E4M3, MT> S;
+    constexpr int P = S::kParts;
+    constexpr int FT = BT / 2 / MT, HN = BN / 4 / MT;            // MT x MT tiles of a wavefront: along t; along half its n
     constexpr int LX = BT / 32, LW = BN / 64;                    // loads (8 rows) of X and of a half of W a wavefront
     // separate arrays: the compiler then knows which loads a read of LDS depends on
     __shared__ i32x4 sx0[BT * 8], sx1[BT * 8], sa0[BN * 4], sa1[BN * 4], sb0[BN * 4], sb1[BN * 4];
     __shared__ float s_scale[E4M3 ? BT : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int g = lane >> 4, r = lane & 15;
+    const int g = lane / MT, r = lane % MT;
 
     // blocks are dealt to the 8 XCDs in turn: give each a contiguous run of
     // tiles, so its L2 serves the rows its blocks share
@@ -293,7 +315,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     }
     const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + n0 * a.ldw, a.ldw, min(BN, a.N - n0), a.chunks);
     const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + t0 * a.ldx, a.ldx, min(BT, a.T - t0), a.chunks);
-    const int lr = lane >> 3, lc = (lane & 7) ^ lr;              // row within a load, chunk of it
+    const int lr = lane >> 3, lc = (lane & 7) ^ ((lr >> 1) + 4 * (wave & 1));   // row within a load, chunk of it
     uint32_t off_x[LX], off_a[LW], off_b[LW];
 #pragma unroll
     for (int i = 0; i < LX; ++i) {
@@ -324,28 +346,31 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
         for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, pb, i, step);
     };
-    const int c0 = g ^ (r & 7), c1 = (g + 4) ^ (r & 7);
+    const int swz = (r >> 1) & 7;
     const int at_x = ((wave & 1) * (BT / 2) + r) * 8, at_w = ((wave >> 1) * (BN / 4) + r) * 8;
-    auto read = [&](const i32x4 *s, int at) { return join(s[at + c0], s[at + c1]); };
-    f32x4 acc[2][FT][HN];
+    auto read = [&](const i32x4 *s, int at, int part) { return S::read(s + at, g, swz, part); };
+    typename S::Acc acc[2][FT][HN];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < FT; ++j)
 #pragma unroll
-            for (int i = 0; i < HN; ++i) acc[h][j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < HN; ++i) acc[h][j][i] = (typename S::Acc)(0.0f);
 
     const int steps = (a.chunks + 7) / 8;
-    i32x8 x[FT], wa[HN], wb[HN];
+    typename S::Operand x[P][FT], wa[P][HN], wb[P][HN];
     fetch_xa(sx0, sa0, 0, LX + LW, 0);
     fetch_b(sb0, 0, LW, 0);
     fetch_xa(sx1, sa1, 0, LX + LW, 1);
     fetch_b(sb1, 0, LW, 1);
     arrive<LX + 3 * LW>();
 #pragma unroll
-    for (int j = 0; j < FT; ++j) x[j] = read(sx0, at_x + j * 128);
+    for (int h = 0; h < P; ++h) {
 #pragma unroll
-    for (int i = 0; i < HN; ++i) wa[i] = read(sa0, at_w + i * 128);
+        for (int j = 0; j < FT; ++j) x[h][j] = read(sx0, at_x + j * (MT * 8), h);
+#pragma unroll
+        for (int i = 0; i < HN; ++i) wa[h][i] = read(sa0, at_w + i * (MT * 8), h);
+    }
     // step k on parts (px, pa, pb), the next step's parts being ox and oa.
     // The scheduling barriers keep each token tile's few loads and reads among
     // its matrix instructions.
@@ -353,20 +378,24 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
         arrive<LX + 2 * LW>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < FT; ++j) {
-            if (j < HN) wb[j] = read(pb, at_w + j * 128);
-            fetch_xa(px, pa, j * (LX + LW) / FT, (j + 1) * (LX + LW) / FT, k + 2);
-            mma<E4M3, HN>(wa, x[j], acc[0][j]);
+        for (int q = 0; q < P * FT; ++q) {
+            const int h = q / FT, j = q % FT;
+            if (q < P * HN) wb[q / HN][q % HN] = read(pb, at_w + q % HN * (MT * 8), q / HN);
+            fetch_xa(px, pa, q * (LX + LW) / (P * FT), (q + 1) * (LX + LW) / (P * FT), k + 2);
+#pragma unroll
+            for (int i = 0; i < HN; ++i) acc[0][j][i] = S::mma(wa[h][i], x[h][j], acc[0][j][i]);
             __builtin_amdgcn_sched_barrier(0);
         }
         arrive<LX + 2 * LW>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < FT; ++j) {
-            if (j < HN) wa[j] = read(oa, at_w + j * 128);
-            fetch_b(pb, j * LW / FT, (j + 1) * LW / FT, k + 2);
-            mma<E4M3, HN>(wb, x[j], acc[1][j]);
-            x[j] = read(ox, at_x + j * 128);
+        for (int q = 0; q < P * FT; ++q) {
+            const int h = q / FT, j = q % FT;
+            if (q < P * HN) wa[q / HN][q % HN] = read(oa, at_w + q % HN * (MT * 8), q / HN);
+            fetch_b(pb, q * LW / (P * FT), (q + 1) * LW / (P * FT), k + 2);
+#pragma unroll
+            for (int i = 0; i < HN; ++i) acc[1][j][i] = S::mma(wb[h][i], x[h][j], acc[1][j][i]);
+            x[h][j] = read(ox, at_x + j * (MT * 8), h);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -379,9 +408,9 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     // Epilogue: the sums pass through LDS, 2 x 16 tokens of a wavefront at a
     // time, so that a lane finishes 8 neighbouring outputs of a token.
     constexpr int CW = BN / 8;                                   // 4-output chunks of a wavefront's row
-    constexpr int PT = BT >= 64 ? 2 : 1;                         // token tiles at a time
-    static_assert(PT * 16 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
-    i32x4 *mine = ((wave & 2) ? sx1 : sx0) + (wave & 1) * (PT * 16 * CW);
+    constexpr int PT = 32 / MT;                                  // token tiles at a time
+    static_assert(32 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
+    i32x4 *mine = ((wave & 2) ? sx1 : sx0) + (wave & 1) * (32 * CW);
     constexpr int LPT = CW / 2, TPI = 64 / LPT;                  // lanes a token, tokens at once
     Columns<E4M3> cols;
     const int lane_n = lane % LPT;
@@ -395,19 +424,23 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
             for (int u = 0; u < PT; ++u)
 #pragma unroll
-                for (int i = 0; i < FN; ++i)
-                    mine[(16 * u + r) * CW + ((4 * i + g) ^ (r & 7))] =
-                        __builtin_bit_cast(i32x4, acc[i / HN][q * PT + u][i % HN]);
+                for (int i = 0; i < 2 * HN; ++i)
+#pragma unroll
+                    for (int c = 0; c < MT / 16 * MT / 16; ++c) {
+                        const typename S::Acc v = acc[i / HN][q * PT + u][i % HN];
+                        mine[(MT * u + r) * CW + ((MT / 4 * i + 2 * c + g) ^ (r & 7))] =
+                            __builtin_bit_cast(i32x4, f32x4{v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]});
+                    }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         // the next token's sums and residuals are asked for before this one's are finished
         int t = lane / LPT;
-        const int t_first = t_wave + p * (16 * PT);
+        const int t_first = t_wave + p * 32;
         half8 res = cols.residual(a, t0 + t_first + t);
         i32x4 lo = mine[t * CW + ((2 * lane_n) ^ (t & 7))], hi = mine[t * CW + ((2 * lane_n + 1) ^ (t & 7))];
 #pragma unroll 1
-        for (; t < 16 * PT; t += TPI) {
-            const int tn = min(t + TPI, 16 * PT - 1);
+        for (; t < 32; t += TPI) {
+            const int tn = min(t + TPI, 31);
             const half8 res_next = cols.residual(a, t0 + t_first + tn);
             const i32x4 lo_next = mine[tn * CW + ((2 * lane_n) ^ (tn & 7))];
             const i32x4 hi_next = mine[tn * CW + ((2 * lane_n + 1) ^ (tn & 7))];
@@ -421,10 +454,10 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     }
 }
 
-template <bool E4M3, int BN, int BT>
+template <bool E4M3, int BN, int BT, int MT>
 __global__ __launch_bounds__(256, BN + BT > 256 ? 1 : 2) void linear_tile_kernel(LinearArgs a, int tiles_n, int tiles_t)
 {
-    linear_tile<E4M3, BN, BT>(a, tiles_n, tiles_t);
+    linear_tile<E4M3, BN, BT, MT>(a, tiles_n, tiles_t);
 }
 
 template <bool E4M3, int FT>
@@ -434,11 +467,11 @@ void launch_stream(const LinearArgs &a, hipStream_t s)
     hipLaunchKernelGGL((linear_stream_kernel<E4M3, FT, 8>), grid, dim3(512), 0, s, a);
 }
 
-template <bool E4M3, int BN, int BT>
+template <bool E4M3, int BN, int BT, int MT>
 void launch_tile(const LinearArgs &a, hipStream_t s)
 {
     const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT;
-    hipLaunchKernelGGL((linear_tile_kernel<E4M3, BN, BT>), dim3((unsigned int)(tn * tt)), dim3(256), 0, s, a, tn, tt);
+    hipLaunchKernelGGL((linear_tile_kernel<E4M3, BN, BT, MT>), dim3((unsigned int)(tn * tt)), dim3(256), 0, s, a, tn, tt);
 }
 
 template <bool E4M3>
@@ -449,9 +482,9 @@ void launch(const LinearArgs &a, hipStream_t s)
     if (a.T <= 64) return launch_stream<E4M3, 4>(a, s);
     const long long big = (long long)((a.N + 255) / 256) * ((a.T + 255) / 256);
     const long long mid = (long long)((a.N + 127) / 128) * ((a.T + 127) / 128);
-    if (big >= 200) return launch_tile<E4M3, 256, 256>(a, s);
-    if (mid >= 200) return launch_tile<E4M3, 128, 128>(a, s);
-    launch_tile<E4M3, 64, 64>(a, s);
+    if (big >= 200) return launch_tile<E4M3, 256, 256, E4M3 ? 16 : 32>(a, s);
+    if (mid >= 200) return launch_tile<E4M3, 128, 128, 16>(a, s);
+    launch_tile<E4M3, 64, 64, 16>(a, s);
 }
 
 constexpr int kMaxLd = 1 << 22;                  // elements: 256 rows stay within 32-bit offsets
