@@ -189,7 +189,9 @@ __device__ inline __amdgpu_buffer_rsrc_t rows_rsrc(const uint8_t *base, long lon
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), (short)0, (int)(uint32_t)bytes, 0x00020000);
 }
 
-constexpr uint32_t kOutside = 0xFFFFFF00u;       // an offset past every buffer: the load returns zeros
+// An offset past every buffer, also with a step's offset along k added: the
+// load returns zeros.
+constexpr uint32_t kOutside = 0xC0000000u;
 
 // ------------------------------------------------------------ few tokens
 // Block: 16 rows of W, FT x 16 tokens, all of k; wavefront w takes the 128-byte
@@ -266,11 +268,11 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 // Block tile BN outputs x BT tokens by 4 wavefronts, 2 x 2, each BN/2 x BT/2 in
 // registers; 128 bytes of k a step.  A step's operands lie in LDS in three
 // parts: the tokens X, and the first and second half (WA, WB) of every
-// wavefront's output rows, each twice (steps k and k + 1).  Per step:
-//     barrier; ask for X, WA of step k + 2; read WB(k); multiply WA(k) . X(k)
-//     barrier; ask for WB of step k + 2; read X, WA of step k + 1; multiply WB(k) . X(k)
+// wavefront's output rows, for B steps at once.  Per step:
+//     barrier; ask for X, WA of step k + B; read WB(k); multiply WA(k) . X(k)
+//     barrier; ask for WB of step k + B; read X, WA of step k + 1; multiply WB(k) . X(k)
 // so a part is overwritten as soon as every wavefront holds it in registers,
-// each load from memory has a step and a half to arrive, and the reads of LDS
+// each load from memory has B - 1/2 steps to arrive, and the reads of LDS
 // run under the matrix instructions: those of the next step's token tile j
 // replace tile j once it has met every row of WB.
 //   A row of a step is 8 chunks of 16 bytes; chunk c of row r sits in slot
@@ -284,15 +286,27 @@ __device__ inline void arrive()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(OUTSTANDING) : "memory");
 }
 
-template <bool E4M3, int BN, int BT, int MT>
+// The parts of stage `STAGE` (0 X, 1 WA, 2 WB), each an LDS array of its own:
+// the compiler then knows which loads a read of LDS depends on.
+template <bool E4M3, int BN, int BT, int MT, int STAGE, int WHICH>
+__device__ inline i32x4 *part()
+{
+    static __shared__ i32x4 s[WHICH == 0 ? BT * 8 : BN * 4];
+    return s;
+}
+
+template <int V>
+struct Const {
+    static constexpr int value = V;
+};
+
+template <bool E4M3, int BN, int BT, int MT, int B>
 __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t)
 {
     typedef Step<E4M3, MT> S;
     constexpr int P = S::kParts;
     constexpr int FT = BT / 2 / MT, HN = BN / 4 / MT;            // MT x MT tiles of a wavefront: along t; along half its n
     constexpr int LX = BT / 32, LW = BN / 64;                    // loads (8 rows) of X and of a half of W a wavefront
-    // separate arrays: the compiler then knows which loads a read of LDS depends on
-    __shared__ i32x4 sx0[BT * 8], sx1[BT * 8], sa0[BN * 4], sa1[BN * 4], sb0[BN * 4], sb1[BN * 4];
     __shared__ float s_scale[E4M3 ? BT : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane / MT, r = lane % MT;
@@ -330,21 +344,20 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     }
     // load i of a part of step `step` (zeros past the last chunk)
     auto fetch = [&](uint32_t off, const __amdgpu_buffer_rsrc_t &rsrc, i32x4 *s, int i, int step) {
-        const bool in = 8 * step + lc < a.chunks && off != kOutside;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(s + (i * 4 + wave) * 64), 16,
-                                                 in ? off + 128u * step : kOutside, 0, 0, 0);
+                                                 8 * step + lc < a.chunks ? off : kOutside, 128 * step, 0, 0);
     };
-    // loads [i0, i1) of X, then WA
-    auto fetch_xa = [&](i32x4 *x, i32x4 *pa, int i0, int i1, int step) {
+    // loads [i0, i1) of X, then WA; of WB
+    auto fetch_xa = [&](auto st, int i0, int i1, int step) {
 #pragma unroll
         for (int i = i0; i < i1; ++i) {
-            if (i < LX) fetch(off_x[i], rx, x, i, step);
-            else fetch(off_a[i - LX], rw, pa, i - LX, step);
+            if (i < LX) fetch(off_x[i], rx, part<E4M3, BN, BT, MT, decltype(st)::value, 0>(), i, step);
+            else fetch(off_a[i - LX], rw, part<E4M3, BN, BT, MT, decltype(st)::value, 1>(), i - LX, step);
         }
     };
-    auto fetch_b = [&](i32x4 *pb, int i0, int i1, int step) {
+    auto fetch_b = [&](auto st, int i0, int i1, int step) {
 #pragma unroll
-        for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, pb, i, step);
+        for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, part<E4M3, BN, BT, MT, decltype(st)::value, 2>(), i, step);
     };
     const int swz = (r >> 1) & 7;
     const int at_x = ((wave & 1) * (BT / 2) + r) * 8, at_w = ((wave >> 1) * (BN / 4) + r) * 8;
@@ -359,49 +372,69 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 
     const int steps = (a.chunks + 7) / 8;
     typename S::Operand x[P][FT], wa[P][HN], wb[P][HN];
-    fetch_xa(sx0, sa0, 0, LX + LW, 0);
-    fetch_b(sb0, 0, LW, 0);
-    fetch_xa(sx1, sa1, 0, LX + LW, 1);
-    fetch_b(sb1, 0, LW, 1);
-    arrive<LX + 3 * LW>();
+    constexpr int STEP = LX + 2 * LW;                            // loads of a step
+    auto fetch_step = [&](auto st) {
+        fetch_xa(st, 0, LX + LW, decltype(st)::value);
+        fetch_b(st, 0, LW, decltype(st)::value);
+    };
+    fetch_step(Const<0>{});
+    fetch_step(Const<1>{});
+    if constexpr (B > 2) fetch_step(Const<2>{});
+    if constexpr (B > 3) fetch_step(Const<3>{});
+    arrive<(B - 1) * STEP + LW>();
 #pragma unroll
     for (int h = 0; h < P; ++h) {
 #pragma unroll
-        for (int j = 0; j < FT; ++j) x[h][j] = read(sx0, at_x + j * (MT * 8), h);
+        for (int j = 0; j < FT; ++j) x[h][j] = read(part<E4M3, BN, BT, MT, 0, 0>(), at_x + j * (MT * 8), h);
 #pragma unroll
-        for (int i = 0; i < HN; ++i) wa[h][i] = read(sa0, at_w + i * (MT * 8), h);
+        for (int i = 0; i < HN; ++i) wa[h][i] = read(part<E4M3, BN, BT, MT, 0, 1>(), at_w + i * (MT * 8), h);
     }
-    // step k on parts (px, pa, pb), the next step's parts being ox and oa.
-    // The scheduling barriers keep each token tile's few loads and reads among
-    // its matrix instructions.
-    auto do_step = [&](int k, i32x4 *px, i32x4 *pa, i32x4 *pb, const i32x4 *ox, const i32x4 *oa) {
-        arrive<LX + 2 * LW>();
+    // Step k, its parts in stage st.  The scheduling barriers keep each token
+    // tile's few loads and reads among its matrix instructions.
+    auto do_step = [&](auto st, int k) {
+        constexpr int ST = decltype(st)::value, NEXT = (ST + 1) % B;
+        arrive<(B - 1) * STEP>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
-            if (q < P * HN) wb[q / HN][q % HN] = read(pb, at_w + q % HN * (MT * 8), q / HN);
-            fetch_xa(px, pa, q * (LX + LW) / (P * FT), (q + 1) * (LX + LW) / (P * FT), k + 2);
+            if (q < P * HN) wb[q / HN][q % HN] = read(part<E4M3, BN, BT, MT, ST, 2>(), at_w + q % HN * (MT * 8), q / HN);
+            fetch_xa(st, q * (LX + LW) / (P * FT), (q + 1) * (LX + LW) / (P * FT), k + B);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[0][j][i] = S::mma(wa[h][i], x[h][j], acc[0][j][i]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        arrive<LX + 2 * LW>();
+        arrive<(B - 1) * STEP>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
-            if (q < P * HN) wa[q / HN][q % HN] = read(oa, at_w + q % HN * (MT * 8), q / HN);
-            fetch_b(pb, q * LW / (P * FT), (q + 1) * LW / (P * FT), k + 2);
+            if (q < P * HN) wa[q / HN][q % HN] = read(part<E4M3, BN, BT, MT, NEXT, 1>(), at_w + q % HN * (MT * 8), q / HN);
+            fetch_b(st, q * LW / (P * FT), (q + 1) * LW / (P * FT), k + B);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[1][j][i] = S::mma(wb[h][i], x[h][j], acc[1][j][i]);
-            x[h][j] = read(ox, at_x + j * (MT * 8), h);
+            x[h][j] = read(part<E4M3, BN, BT, MT, NEXT, 0>(), at_x + j * (MT * 8), h);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    for (int k = 0; k < steps; k += 2) {                         // an odd last step is followed by one of zeros
-        do_step(k, sx0, sa0, sb0, sx1, sa1);
-        do_step(k + 1, sx1, sa1, sb1, sx0, sa0);
+    if constexpr (B == 2) {
+        for (int k = 0; k < steps; k += 2) {                     // an odd last step is followed by one of zeros
+            do_step(Const<0>{}, k);
+            do_step(Const<1>{}, k + 1);
+        }
+    } else {
+        for (int k = 0;; k += B) {
+            do_step(Const<0>{}, k);
+            if (k + 1 >= steps) break;
+            do_step(Const<1>{}, k + 1);
+            if (k + 2 >= steps) break;
+            do_step(Const<2>{}, k + 2);
+            if (k + 3 >= steps) break;
+            if constexpr (B > 3) {
+                do_step(Const<3>{}, k + 3);
+                if (k + 4 >= steps) break;
+            }
+        }
     }
     arrive<0>();                                                 // no load is on its way to LDS any more
 
@@ -410,7 +443,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     constexpr int CW = BN / 8;                                   // 4-output chunks of a wavefront's row
     constexpr int PT = 32 / MT;                                  // token tiles at a time
     static_assert(32 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
-    i32x4 *mine = ((wave & 2) ? sx1 : sx0) + (wave & 1) * (32 * CW);
+    i32x4 *mine = ((wave & 2) ? part<E4M3, BN, BT, MT, 1, 0>() : part<E4M3, BN, BT, MT, 0, 0>()) + (wave & 1) * (32 * CW);
     constexpr int LPT = CW / 2, TPI = 64 / LPT;                  // lanes a token, tokens at once
     Columns<E4M3> cols;
     const int lane_n = lane % LPT;
@@ -454,10 +487,10 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     }
 }
 
-template <bool E4M3, int BN, int BT, int MT>
+template <bool E4M3, int BN, int BT, int MT, int B>
 __global__ __launch_bounds__(256, BN + BT > 256 ? 1 : 2) void linear_tile_kernel(LinearArgs a, int tiles_n, int tiles_t)
 {
-    linear_tile<E4M3, BN, BT, MT>(a, tiles_n, tiles_t);
+    linear_tile<E4M3, BN, BT, MT, B>(a, tiles_n, tiles_t);
 }
 
 template <bool E4M3, int FT>
@@ -467,11 +500,11 @@ void launch_stream(const LinearArgs &a, hipStream_t s)
     hipLaunchKernelGGL((linear_stream_kernel<E4M3, FT, 8>), grid, dim3(512), 0, s, a);
 }
 
-template <bool E4M3, int BN, int BT, int MT>
+template <bool E4M3, int BN, int BT, int MT, int B>
 void launch_tile(const LinearArgs &a, hipStream_t s)
 {
     const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT;
-    hipLaunchKernelGGL((linear_tile_kernel<E4M3, BN, BT, MT>), dim3((unsigned int)(tn * tt)), dim3(256), 0, s, a, tn, tt);
+    hipLaunchKernelGGL((linear_tile_kernel<E4M3, BN, BT, MT, B>), dim3((unsigned int)(tn * tt)), dim3(256), 0, s, a, tn, tt);
 }
 
 template <bool E4M3>
@@ -482,9 +515,10 @@ void launch(const LinearArgs &a, hipStream_t s)
     if (a.T <= 64) return launch_stream<E4M3, 4>(a, s);
     const long long big = (long long)((a.N + 255) / 256) * ((a.T + 255) / 256);
     const long long mid = (long long)((a.N + 127) / 128) * ((a.T + 127) / 128);
-    if (big >= 200) return launch_tile<E4M3, 256, 256, E4M3 ? 16 : 32>(a, s);
-    if (mid >= 200) return launch_tile<E4M3, 128, 128, 16>(a, s);
-    launch_tile<E4M3, 64, 64, 16>(a, s);
+    if (big >= 200) return launch_tile<E4M3, 256, 256, E4M3 ? 16 : 32, 2>(a, s);
+    if (mid > 256) return launch_tile<E4M3, 128, 128, E4M3 ? 16 : 32, 2>(a, s);
+    if (mid >= 128) return launch_tile<E4M3, 128, 128, E4M3 ? 16 : 32, 4>(a, s);
+    launch_tile<E4M3, 64, 64, 16, 4>(a, s);
 }
 
 constexpr int kMaxLd = 1 << 22;                  // elements: 256 rows stay within 32-bit offsets
