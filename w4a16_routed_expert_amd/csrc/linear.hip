@@ -269,10 +269,11 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 // registers; 128 bytes of k a step.  A step's operands lie in LDS in three
 // parts: the tokens X, and the first and second half (WA, WB) of every
 // wavefront's output rows, for B steps at once.  Per step:
-//     barrier; ask for X, WA of step k + B; read WB(k); multiply WA(k) . X(k)
-//     barrier; ask for WB of step k + B; read X, WA of step k + 1; multiply WB(k) . X(k)
-// so a part is overwritten as soon as every wavefront holds it in registers,
-// each load from memory has B - 1/2 steps to arrive, and the reads of LDS
+//     barrier; ask for WB of step k + B - 1; read WB(k); multiply WA(k) . X(k)
+//     barrier; ask for X, WA of step k + B; read X, WA of step k + 1; multiply WB(k) . X(k)
+// A part is overwritten after the barrier that follows the products it was
+// read for: every wavefront's reads of it have then returned, so the barriers
+// wait for loads from memory only.  Each load has B - 1 steps to arrive, and the reads of LDS
 // run under the matrix instructions: those of the next step's token tile j
 // replace tile j once it has met every row of WB.
 //   A row of a step is 8 chunks of 16 bytes; chunk c of row r sits in slot
@@ -282,8 +283,8 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 template <int OUTSTANDING>
 __device__ inline void arrive()
 {
-    // this wavefront's older loads have landed and its reads are in registers, then everyone's
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"i"(OUTSTANDING) : "memory");
+    // all but the newest of this wavefront's loads have landed in LDS, then everyone's
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"i"(OUTSTANDING) : "memory");
 }
 
 // The parts of stage `STAGE` (0 X, 1 WA, 2 WB), each an LDS array of its own:
@@ -372,16 +373,19 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 
     const int steps = (a.chunks + 7) / 8;
     typename S::Operand x[P][FT], wa[P][HN], wb[P][HN];
-    constexpr int STEP = LX + 2 * LW;                            // loads of a step
-    auto fetch_step = [&](auto st) {
-        fetch_xa(st, 0, LX + LW, decltype(st)::value);
-        fetch_b(st, 0, LW, decltype(st)::value);
-    };
-    fetch_step(Const<0>{});
-    fetch_step(Const<1>{});
-    if constexpr (B > 2) fetch_step(Const<2>{});
-    if constexpr (B > 3) fetch_step(Const<3>{});
-    arrive<(B - 1) * STEP + LW>();
+    constexpr int XA = LX + LW;
+    fetch_xa(Const<0>{}, 0, XA, 0);
+    fetch_b(Const<0>{}, 0, LW, 0);
+    fetch_xa(Const<1>{}, 0, XA, 1);
+    if constexpr (B > 2) {
+        fetch_b(Const<1>{}, 0, LW, 1);
+        fetch_xa(Const<2>{}, 0, XA, 2);
+    }
+    if constexpr (B > 3) {
+        fetch_b(Const<2>{}, 0, LW, 2);
+        fetch_xa(Const<3>{}, 0, XA, 3);
+    }
+    arrive<(B - 1) * (XA + LW)>();
 #pragma unroll
     for (int h = 0; h < P; ++h) {
 #pragma unroll
@@ -392,25 +396,25 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     // Step k, its parts in stage st.  The scheduling barriers keep each token
     // tile's few loads and reads among its matrix instructions.
     auto do_step = [&](auto st, int k) {
-        constexpr int ST = decltype(st)::value, NEXT = (ST + 1) % B;
-        arrive<(B - 1) * STEP>();
+        constexpr int ST = decltype(st)::value, NEXT = (ST + 1) % B, LAST = (ST + B - 1) % B;
+        arrive<(B - 1) * XA + (B - 2) * LW>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
             if (q < P * HN) wb[q / HN][q % HN] = read(part<E4M3, BN, BT, MT, ST, 2>(), at_w + q % HN * (MT * 8), q / HN);
-            fetch_xa(st, q * (LX + LW) / (P * FT), (q + 1) * (LX + LW) / (P * FT), k + B);
+            fetch_b(Const<LAST>{}, q * LW / (P * FT), (q + 1) * LW / (P * FT), k + B - 1);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[0][j][i] = S::mma(wa[h][i], x[h][j], acc[0][j][i]);
             __builtin_amdgcn_sched_barrier(0);
         }
-        arrive<(B - 1) * STEP>();
+        arrive<(B - 2) * XA + (B - 1) * LW>();
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
             if (q < P * HN) wa[q / HN][q % HN] = read(part<E4M3, BN, BT, MT, NEXT, 1>(), at_w + q % HN * (MT * 8), q / HN);
-            fetch_b(st, q * LW / (P * FT), (q + 1) * LW / (P * FT), k + B);
+            fetch_xa(st, q * XA / (P * FT), (q + 1) * XA / (P * FT), k + B);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[1][j][i] = S::mma(wb[h][i], x[h][j], acc[1][j][i]);
             x[h][j] = read(part<E4M3, BN, BT, MT, NEXT, 0>(), at_x + j * (MT * 8), h);
