@@ -91,7 +91,7 @@ class Call:
             got[name] = t[:self.n[name]].cpu().numpy()
         got["ids"], got["w"] = got["ids"].reshape(self.T, self.k), got["w"].reshape(self.T, self.k)
         got["logits"] = got["logits"].reshape(self.T, self.E)
-        assert int(self.ws[:256].sum()) == 0, "the counter is left nonzero"
+        assert int(self.ws[:1024].sum()) == 0, "the counter is left nonzero"
         return got
 
 
@@ -125,7 +125,8 @@ RULES = [dict(score=SOFTMAX, renorm=False), dict(score=SIGMOID, scale=2.5),
 @pytest.mark.parametrize("rule", RULES, ids=["softmax", "sigmoid", "sigmoid-groups", "softmax-groups"])
 @pytest.mark.parametrize("T,H,E,k", [(1, 128, 8, 2), (1, 2048, 64, 8), (5, 384, 12, 4), (32, 2048, 64, 8),
                                      (64, 1408, 60, 4), (65, 256, 16, 3), (80, 128, 32, 8), (97, 640, 60, 4),
-                                     (129, 4096, 24, 5), (333, 2048, 64, 8), (1000, 256, 36, 6)])
+                                     (129, 4096, 24, 5), (333, 2048, 64, 8), (1000, 256, 36, 6),
+                                     (1040, 384, 64, 8), (1041, 256, 20, 4), (2048, 128, 64, 4), (2049, 256, 40, 8)])
 def test_equals_the_definition(T, H, E, k, rule):
     x, wr, bias = inputs(T, H, E)
     xd, wd, bd = device(x, wr, bias)
@@ -250,7 +251,7 @@ def test_selection_does_not_depend_on_the_batch():
         assert np.array_equal(a[name][100:140], b[name]), name
 
 
-@pytest.mark.parametrize("T", [16, 160])
+@pytest.mark.parametrize("T", [1, 16, 160, 1200])
 def test_captured_replays(T):
     H, E, k = 512, 64, 8
     rule = dict(score=SIGMOID, n_group=8, topk_group=4, group=TOP2, scale=2.5)

@@ -15,10 +15,12 @@
 // choice values and group values are in fp64, so a selection does not depend
 // on summation order or batch size.
 //
-// Small batches: one launch as in the fused layer (a block per token and 16
-// experts; the block that finishes last selects and groups).  Larger ones:
-// route_tile_kernel computes 16 tokens x all experts per block with the fp64
-// matrix instruction and selects at once, then one launch places the pairs.
+// Small batches: one launch, a block per token and 16 experts; the block that
+// completes a token's logits selects its experts, the one that completes the
+// batch groups the pairs.  Larger ones: route_tile_kernel computes the logits of
+// 16 tokens with the fp64 matrix instruction (the experts divided among blocks
+// while there are too few tiles for the GPU) and the block that completes a
+// tile selects; then one launch places the pairs.  No block waits for another.
 #include "moe_internal.h"
 
 #include <climits>
@@ -88,10 +90,16 @@ __device__ inline void select_wave(const ScoreRule &rule, int E, int k, int lane
         S.c[lane] = c;
         double best = -INFINITY, second = -INFINITY;
         if (lane < rule.n_group) {
-            for (int i = 0; i < gs; ++i) {
-                const double v = S.c[lane * gs + i];
-                second = fmax(second, fmin(best, v));
-                best = fmax(best, v);
+            for (int i0 = 0; i0 < gs; i0 += 4) {               // four reads in flight
+                double v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = S.c[lane * gs + min(i0 + i, gs - 1)];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i0 + i >= gs) break;
+                    second = fmax(second, fmin(best, v[i]));
+                    best = fmax(best, v[i]);
+                }
             }
         }
         double value = rule.top2 ? best + second : best;
@@ -131,55 +139,69 @@ __device__ inline void select_wave(const ScoreRule &rule, int E, int k, int lane
 }
 
 // ------------------------------------------------------------ small batches: one launch
+constexpr int kScoredSmallT = 64;            // largest batch routed in one launch
+
 union SmallLds {
     LogitsLds lg;
     struct {
         GroupLds<kSelWaves, true> gr;
-        SelectLds sel[kSelWaves];
+        SelectLds sel;
     } g;
 };
 
+// done[t]: blocks that have stored their logits of token t; done[kScoredSmallT]:
+// tokens selected.  All zero before and after the call.
 template <int VEC>
 __global__ __launch_bounds__(kSelThreads) void route_scored_small_kernel(RouteArgs a, ScoreRule rule,
                                                                          unsigned int *done)
 {
     __shared__ SmallLds S;
-    __shared__ int s_last;
+    __shared__ int s_last, s_all;
     const int G = (a.E + kGroupE - 1) / kGroupE;
-    logits_block<VEC, true, true>(a, S.lg, blockIdx.x / G, blockIdx.x % G);
+    const int t = blockIdx.x / G, lane = threadIdx.x & 63;
+    logits_block<VEC, true, true>(a, S.lg, t, blockIdx.x % G);
     moe::wait_stores();                                     // this wave's logits are complete
     __syncthreads();
     if (threadIdx.x == 0) {
-        const unsigned int before = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = before == gridDim.x - 1;
+        const unsigned int before = __hip_atomic_fetch_add(&done[t], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = before == (unsigned int)G - 1;
     }
     __syncthreads();
     if (!s_last) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int t = wave; t < a.T; t += kSelWaves) {
+    if (threadIdx.x < 64) {
         const float lv = moe::load_dev(a.lbuf + (size_t)t * a.E + min(lane, a.E - 1));
-        if (a.logits && lane < a.E) a.logits[(size_t)t * a.E + lane] = lv;
         int id;
         float w;
-        select_wave(rule, a.E, a.k, lane, lv, S.g.sel[wave], id, w);
+        select_wave(rule, a.E, a.k, lane, lv, S.g.sel, id, w);
+        if (a.logits && lane < a.E) a.logits[(size_t)t * a.E + lane] = lv;
         if (lane < a.k) {
-            const size_t p = (size_t)t * a.k + lane;
-            a.ids[p] = id;
-            a.w[p] = w;
-            S.g.gr.ids[p] = id;
+            moe::store_dev(&a.ids[(size_t)t * a.k + lane], (int32_t)id);
+            a.w[(size_t)t * a.k + lane] = w;
+        }
+        moe::wait_stores();                                 // the ids are complete
+        if (lane == 0) {
+            done[t] = 0u;
+            unsigned int *all = done + kScoredSmallT;
+            const unsigned int before =
+                a.T == 1 ? 0u : __hip_atomic_fetch_add(all, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s_all = before == (unsigned int)a.T - 1;
+            if (s_all && a.T > 1) *all = 0u;
         }
     }
     __syncthreads();
+    if (!s_all) return;
+    for (int p = threadIdx.x; p < a.T * a.k; p += kSelThreads) S.g.gr.ids[p] = moe::load_dev(&a.ids[p]);
+    __syncthreads();
     group_sort<kSelWaves, true, false>(a, S.g.gr);
-    if (threadIdx.x == 0) *done = 0u;
 }
 
 // ------------------------------------------------------------ larger batches
-// Block: 16 tokens x all experts.  Its 8 wavefronts split H; a wavefront's step
+// Block: 16 tokens x 16 NT experts.  Its 8 wavefronts split H; a wavefront's step
 // takes 32 values of H: lane 16q + j holds 8 of token j (values 8q .. 8q + 7 of
 // the step) and, per value, the NT experts NT*j .. NT*j + NT - 1 of that router
 // row, so one load of NT experts feeds NT matrix instructions (tile n's column
-// j is expert NT*j + n; the columns are a permutation of the experts).
+// j is expert NT*j + n; the columns are a permutation of the experts).  The
+// loads of a step are in flight while the one before it is multiplied.
 //   fp64 matrix instruction, 16x16x4: the products of FP16 values are exact in
 //   fp64; a wavefront's chain has H/8 additions per output and the 8 partial
 //   sums are added in order: at most H/8 + 8 additions on a path.
@@ -197,18 +219,47 @@ struct TileLds {
     long long ered[kSelWaves][2];
     SelectLds sel[kSelWaves];
     int cnt[MOE_MAX_EXPERTS];
+    int last;
 };
 
+// One step's operands of a lane.
 template <int NT, bool WIDE>
-__global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, ScoreRule rule, int *counts)
+struct TileStep {
+    typename WLoad<8>::T x;
+    typename WLoad<NT>::T w[8];
+    uint16_t w1[8][WIDE ? 1 : NT];
+
+    // wide: the lane's NT experts lie in one aligned word; else `m` of them, singly
+    __device__ inline void load(const uint16_t *xrow, const uint16_t *wcol, int h, int E, int m)
+    {
+        x = WLoad<8>::ld(xrow + h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint16_t *row = wcol + (size_t)(h + i) * E;
+            if constexpr (WIDE) {
+                w[i] = WLoad<NT>::ld(row);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) w1[i][n] = row[min(n, m - 1)];
+            }
+        }
+    }
+    __device__ inline uint16_t weight(int i, int n) const { return WIDE ? WLoad<NT>::get(w[i], n) : w1[i][WIDE ? 0 : n]; }
+};
+
+// Grid: tiles x parts (part p: experts 16 NT p and on).  With more than one
+// part the logits meet in a.lbuf ([T][E], device scope) and done[tile] counts
+// the parts stored (zero before and after).  counts[tile][E]: the tile's pairs per expert.
+template <int NT, bool WIDE>
+__global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, ScoreRule rule, int *counts,
+                                                                 unsigned int *done)
 {
     __shared__ TileLds<NT> S;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int E = a.E, H = a.H, T = a.T, k = a.k;
-    const int t0 = blockIdx.x * kTileT;
+    const int tile = blockIdx.x, t0 = tile * kTileT;
+    const int first = blockIdx.y * (16 * NT), mine = min(E - first, 16 * NT);   // this block's experts
     const int j = lane & 15, q = lane >> 4;
-    typedef WLoad<8> XL;
-    typedef WLoad<NT> L;
 
     f64x4 acc[NT];
     float wsq[NT], xsq = 0.0f;
@@ -218,34 +269,24 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         wsq[n] = 0.0f;
     }
     const uint16_t *xrow = a.x + (size_t)min(t0 + j, T - 1) * H + 8 * q;
-    const int e0 = NT * j < E ? NT * j : 0;          // lanes past the experts repeat expert 0 (their columns are not read)
-    const uint16_t *wcol = a.wr + e0;
+    const int e0 = NT * j < mine ? NT * j : 0;       // lanes past the experts repeat the first (their columns are not read)
+    const uint16_t *wcol = a.wr + (size_t)(8 * q) * E + first + e0;
+    TileStep<NT, WIDE> cur, nxt;
+    if (32 * wave < H) cur.load(xrow, wcol, 32 * wave, E, mine - e0);
     for (int h0 = 32 * wave; h0 < H; h0 += 32 * kSelWaves) {
-        const typename XL::T xv = XL::ld(xrow + h0);
-        uint16_t wv[8][NT];
+        if (h0 + 32 * kSelWaves < H) nxt.load(xrow, wcol, h0 + 32 * kSelWaves, E, mine - e0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint16_t *row = wcol + (size_t)(h0 + 8 * q + i) * E;
-            if constexpr (WIDE) {
-                const typename L::T v = L::ld(row);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) wv[i][n] = L::get(v, n);
-            } else {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) wv[i][n] = row[min(n, E - 1 - e0)];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float xf = (float)__builtin_bit_cast(_Float16, XL::get(xv, i));
+            const float xf = (float)__builtin_bit_cast(_Float16, WLoad<8>::get(cur.x, i));
             xsq = fmaf(xf, xf, xsq);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float wf = (float)__builtin_bit_cast(_Float16, wv[i][n]);
+                const float wf = (float)__builtin_bit_cast(_Float16, cur.weight(i, n));
                 wsq[n] = fmaf(wf, wf, wsq[n]);
                 acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)xf, (double)wf, acc[n], 0, 0, 0);
             }
         }
+        cur = nxt;
     }
     // partial sums of this wavefront: lane (q, j) holds tokens q + 4r of column j
 #pragma unroll
@@ -263,12 +304,12 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
     if (tid < kTileT) S.redo[tid] = 0ull;
     if (tid < MOE_MAX_EXPERTS) S.cnt[tid] = 0;
     __syncthreads();
-    constexpr int PER = kTileT * NT * 16 / kSelThreads > 0 ? kTileT * NT * 16 / kSelThreads : 1;
+    constexpr int OUT = kTileT * NT * 16;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int o = tid + i * kSelThreads;
+    for (int o0 = 0; o0 < OUT; o0 += kSelThreads) {
+        const int o = o0 + tid;
         const int tt = o / (NT * 16), e = o % (NT * 16);
-        if (tt >= kTileT || e >= E || t0 + tt >= T) continue;
+        if (o >= OUT || e >= mine || t0 + tt >= T) continue;
         double v = 0.0;
         float X = 0.0f, W = 0.0f;
 #pragma unroll
@@ -283,7 +324,7 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         const double err = (double)(H / kSelWaves + kSelWaves + 1) * 0x1p-53 * sqrt((double)X * (double)W) *
                            (1.0 + 0x1p-9);
         S.logit[tt][e] = (float)v;
-        if (isfinite(v) && (a.force_exact || !rn32_certain(v, err))) atomicOr(&S.redo[tt], 1ull << e);
+        if (isfinite(v) && !rn32_certain(v, err)) atomicOr(&S.redo[tt], 1ull << e);
     }
     __syncthreads();
     for (int tt = 0; tt < kTileT; ++tt) {
@@ -291,15 +332,33 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         while (redo) {                               // rare: exact recomputation by the whole block
             const int e = __builtin_ctzll(redo);
             redo &= redo - 1ull;
-            const float l = exact_logit(a, reinterpret_cast<const _Float16 *>(a.x) + (size_t)(t0 + tt) * H, e, S.ered);
+            const float l = exact_logit(a, reinterpret_cast<const _Float16 *>(a.x) + (size_t)(t0 + tt) * H, first + e,
+                                        S.ered);
             if (tid == 0) S.logit[tt][e] = l;
         }
     }
     __syncthreads();
+    if (gridDim.y > 1) {
+        for (int o = tid; o < OUT; o += kSelThreads) {
+            const int tt = o / (NT * 16), e = o % (NT * 16);
+            if (e < mine && t0 + tt < T) moe::store_dev(&a.lbuf[(size_t)(t0 + tt) * E + first + e], S.logit[tt][e]);
+        }
+        moe::wait_stores();
+        __syncthreads();
+        if (tid == 0) {
+            const unsigned int before =
+                __hip_atomic_fetch_add(&done[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            S.last = before == gridDim.y - 1;
+            if (S.last) done[tile] = 0u;
+        }
+        __syncthreads();
+        if (!S.last) return;
+    }
     for (int tt = wave; tt < kTileT; tt += kSelWaves) {
         const int t = t0 + tt;
         if (t >= T) break;
-        const float lv = S.logit[tt][min(lane, E - 1)];
+        const int e = min(lane, E - 1);
+        const float lv = gridDim.y > 1 ? moe::load_dev(&a.lbuf[(size_t)t * E + e]) : S.logit[tt][e];
         if (a.logits && lane < E) a.logits[(size_t)t * E + lane] = lv;
         int id;
         float w;
@@ -312,7 +371,7 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         }
     }
     __syncthreads();
-    if (tid < E) counts[(size_t)blockIdx.x * E + tid] = S.cnt[tid];
+    if (tid < E) counts[(size_t)tile * E + tid] = S.cnt[tid];
 }
 
 // Places the pairs of `tiles` 16-token tiles per block: expert e's pairs of
@@ -392,23 +451,34 @@ __global__ __launch_bounds__(kPlaceWaves * 64) void route_place_kernel(RouteArgs
     }
 }
 
-constexpr int kScoredSmallT = 64;            // largest batch routed in one launch
-constexpr size_t kScoredCtrl = 256;          // the counter, before the logits or counts
+// Tiles whose experts are divided among blocks: enough blocks for the GPU's
+// 256 CUs.
+constexpr int kSplitTiles = 128;
+
+// Workspace: the counters (zero between calls), then the logits handed between
+// blocks, then the tiles' counts.
+constexpr size_t kScoredCtrl = 1024;
+static_assert(kScoredCtrl >= (kScoredSmallT + 1) * sizeof(int) && kScoredCtrl >= kSplitTiles * sizeof(int), "counters");
+
+size_t scored_lbuf_bytes(int T, int E)
+{
+    const int rows = T < kSplitTiles * kTileT ? T : kSplitTiles * kTileT;
+    return ((size_t)rows * E * sizeof(float) + 255) / 256 * 256;
+}
 
 size_t scored_ws_bytes(int T, int E)
 {
-    const size_t lbuf = (size_t)(T < kScoredSmallT ? T : kScoredSmallT) * E * sizeof(float);
     const size_t counts = (size_t)((T + kTileT - 1) / kTileT) * E * sizeof(int);
-    return kScoredCtrl + ((lbuf > counts ? lbuf : counts) + 255) / 256 * 256;
+    return kScoredCtrl + scored_lbuf_bytes(T, E) + (counts + 255) / 256 * 256;
 }
 
 template <int NT>
-void launch_tiles(const RouteArgs &a, const ScoreRule &rule, int *counts, hipStream_t s)
+void launch_tiles(const RouteArgs &a, const ScoreRule &rule, int *counts, unsigned int *done, hipStream_t s)
 {
-    const dim3 grid((unsigned int)((a.T + kTileT - 1) / kTileT));
+    const dim3 grid((unsigned int)((a.T + kTileT - 1) / kTileT), (unsigned int)((a.E + 16 * NT - 1) / (16 * NT)));
     if (a.E % NT == 0 && moe::aligned(a.wr, 2 * NT))
-        hipLaunchKernelGGL((route_tile_kernel<NT, true>), grid, dim3(kSelThreads), 0, s, a, rule, counts);
-    else hipLaunchKernelGGL((route_tile_kernel<NT, false>), grid, dim3(kSelThreads), 0, s, a, rule, counts);
+        hipLaunchKernelGGL((route_tile_kernel<NT, true>), grid, dim3(kSelThreads), 0, s, a, rule, counts, done);
+    else hipLaunchKernelGGL((route_tile_kernel<NT, false>), grid, dim3(kSelThreads), 0, s, a, rule, counts, done);
 }
 
 }  // namespace
@@ -491,13 +561,16 @@ int moe_route_scored(const void *x_dev, const void *w_router_dev, const float *s
         else hipLaunchKernelGGL(route_scored_small_kernel<1>, dim3(blocks), dim3(kSelThreads), 0, s, a, r, done);
         return moe::check_launch(who);
     }
-    int *counts = (int *)a.lbuf;
-    if (E <= 16) launch_tiles<1>(a, r, counts, s);
-    else if (E <= 32) launch_tiles<2>(a, r, counts, s);
-    else launch_tiles<4>(a, r, counts, s);
+    int *counts = (int *)((uint8_t *)a.lbuf + scored_lbuf_bytes(T, E));
+    unsigned int *done = (unsigned int *)ws_dev;
+    const int tiles_total = (T + kTileT - 1) / kTileT;
+    // one block has the tile's experts where that fills the GPU, else 2 or 4 divide them
+    const int column_tiles = (E + 15) / 16;
+    if (column_tiles > 2 && tiles_total > kSplitTiles) launch_tiles<4>(a, r, counts, done, s);
+    else if (column_tiles > 1 && tiles_total > kSplitTiles / 2) launch_tiles<2>(a, r, counts, done, s);
+    else launch_tiles<1>(a, r, counts, done, s);
     rc = moe::check_launch("moe_route_scored (select)");
     if (rc) return rc;
-    const int tiles_total = (T + kTileT - 1) / kTileT;
     // at least 4 tiles per block, and at most 256 blocks: every block reads all tiles' counts
     const int tiles = tiles_total > 1024 ? (tiles_total + 255) / 256 : 4;
     hipLaunchKernelGGL(route_place_kernel, dim3((unsigned int)((tiles_total + tiles - 1) / tiles)),
