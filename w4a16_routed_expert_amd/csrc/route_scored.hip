@@ -35,38 +35,47 @@ struct ScoreRule {
     double scale;
 };
 
-// LDS of one wavefront's selection.
+// LDS of one wavefront's selection.  A wavefront's LDS operations complete in
+// order, so its lanes exchange values through it without a barrier.
 struct SelectLds {
-    double c[64];
+    double s[64], c[64];     // scores, choice values
+    double top[2][64];       // a group's two largest choice values
+    double value[64];        // group values
+    int key[64];             // choice values rounded to FP32, as ordered integers
+    int slot[MOE_MAX_TOPK];  // expert + 1 of each slot
 };
 
-__device__ inline double lane_value(double v, int src)
+// The value of lane 0 for all (lanes add in different orders: one lane's sum
+// keeps equal logits at equal scores).
+__device__ inline double first_lane(double v)
 {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, src);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), src);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
     return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
 }
 
-// How many of the first n lanes hold a larger value, or an equal one and a
-// lower lane (lanes of the mask `in` only).
-__device__ inline int rank_of(double v, int lane, int n, unsigned long long in)
+// How many of v[0 .. n) are above x, or equal to it and before place `at`.
+__device__ inline int rank_among(const double *v, int n, double x, int at)
 {
     int rank = 0;
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
-        if (!((in >> i) & 1ull)) continue;
-        const double o = lane_value(v, i);
-        rank += (o > v || (o == v && i < lane)) ? 1 : 0;
+        const double o = v[i];
+        rank += (o > x || (o == x && i < at)) ? 1 : 0;
     }
     return rank;
 }
 
 // Scores, choice and weights of one token by one wavefront (lane = expert, lv
-// its logit).  Lane j < k ends with slot j's expert and weight.
+// its logit).  Lane j < k ends with slot j's expert and weight.  Bound by the
+// latency of its chain of steps, so ranks are counted against values read from
+// LDS (all reads in flight) rather than found by rounds of wavefront maxima.
 //
-// The k rounds compare the FP32 roundings of the choice values, which keep
-// their order except that different values may become equal: only when a
-// round's maximum is held by more than one lane are the fp64 values ranked.
+// The ranks compare the FP32 roundings of the choice values, which keep their
+// order except that different values may become equal: only then (a slot
+// without an expert, or more than k experts ranked below k) are the fp64
+// values ranked.
 __device__ inline void select_wave(const ScoreRule &rule, int E, int k, int lane, float lv, SelectLds &S, int &id,
                                    float &weight)
 {
@@ -76,64 +85,59 @@ __device__ inline void select_wave(const ScoreRule &rule, int E, int k, int lane
         const int top = wave_max(lane < E ? order_key(lv) : INT_MIN);
         const float mx = __builtin_bit_cast(float, top ^ ((top >> 31) & 0x7FFFFFFF));
         const double e = lane < E ? exp(l - (double)mx) : 0.0;
-        // one lane's sum for all: lanes add in different orders, and equal logits have equal scores
-        s = e / lane_value(sum_phases<1>(e), 0);
+        s = e / first_lane(sum_phases<1>(e));
     } else {
         s = 1.0 / (1.0 + exp(-l));
     }
     double c = s;
     if (rule.bias) c += (double)rule.bias[min(lane, E - 1)];
     if (isnan(c)) c = -INFINITY;
-    unsigned long long in = E == 64 ? ~0ull : (1ull << E) - 1ull;
+    S.s[lane] = s;
+    S.c[lane] = c;
+    bool in = lane < E;
     if (rule.n_group > 1) {
-        const int gs = E / rule.n_group;
-        S.c[lane] = c;
-        double best = -INFINITY, second = -INFINITY;
-        if (lane < rule.n_group) {
-            for (int i0 = 0; i0 < gs; i0 += 4) {               // four reads in flight
-                double v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = S.c[lane * gs + min(i0 + i, gs - 1)];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i0 + i >= gs) break;
-                    second = fmax(second, fmin(best, v[i]));
-                    best = fmax(best, v[i]);
-                }
-            }
+        const int gs = E / rule.n_group, g = min(lane / gs, rule.n_group - 1), m = lane - g * gs;
+        const int r = rank_among(&S.c[g * gs], gs, c, m);
+        if (in && r < 2) S.top[r][g] = c;
+        if (in && r == 0) {
+            double v = S.top[0][g];
+            if (rule.top2) v += S.top[1][g];
+            S.value[g] = isnan(v) ? -INFINITY : v;
         }
-        double value = rule.top2 ? best + second : best;
-        if (isnan(value)) value = -INFINITY;
-        const unsigned long long all = rule.n_group == 64 ? ~0ull : (1ull << rule.n_group) - 1ull;
-        const int rank = rank_of(value, lane, rule.n_group, all);
-        const unsigned long long kept = __ballot(lane < rule.n_group && rank < rule.topk_group);
-        in = __ballot(lane < E && ((kept >> (lane / gs)) & 1ull));
+        in = in && rank_among(S.value, rule.n_group, S.value[g], g) < rule.topk_group;
     }
-    int key = ((in >> lane) & 1ull) ? order_key((float)c) : INT_MIN;
-    bool tie = false;
-    id = 0;
-    for (int j = 0; j < k; ++j) {
-        const int m = wave_max(key);
-        const unsigned long long who = __ballot(key == m);
-        const int win = (int)__builtin_ctzll(who);
-        tie = tie || (who & (who - 1ull));
-        if (lane == win) key = INT_MIN;
-        if (lane == j) id = win;
+    const int key = in ? order_key((float)c) : INT_MIN;
+    S.key[lane] = key;
+    if (lane < MOE_MAX_TOPK) S.slot[lane] = 0;
+    int rank = 0;
+    const int4 *keys = reinterpret_cast<const int4 *>(S.key);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int4 o = keys[i];
+        rank += (o.x > key ? 1 : 0) + (o.y > key ? 1 : 0) + (o.z > key ? 1 : 0) + (o.w > key ? 1 : 0);
     }
-    if (tie) {
-        const int rank = rank_of(c, lane, E, in);
-        for (int j = 0; j < k; ++j) {
-            const unsigned long long who = __ballot(((in >> lane) & 1ull) && rank == j);
-            if (lane == j) id = (int)__builtin_ctzll(who);
+    const bool chosen = in && rank < k;
+    if (chosen) S.slot[rank] = lane + 1;
+    id = S.slot[min(lane, MOE_MAX_TOPK - 1)] - 1;
+    if (__popcll(__ballot(chosen)) != k || __ballot(lane < k && id < 0)) {
+        S.c[lane] = in ? c : -INFINITY;
+        rank = 0;
+        for (int i = 0; i < E; ++i) {
+            const double o = S.c[i];
+            // an expert left out ranks after one whose value is -infinity
+            if (S.key[i] != INT_MIN) rank += (o > c || (o == c && i < lane)) ? 1 : 0;
         }
+        if (in && rank < k) S.slot[rank] = lane + 1;
+        id = S.slot[min(lane, MOE_MAX_TOPK - 1)] - 1;
     }
-    const uint64_t sb = __builtin_bit_cast(uint64_t, s);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * id, (int)(uint32_t)sb);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * id, (int)(uint32_t)(sb >> 32));
-    double w = __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+    double w = S.s[max(id, 0)];
     if (rule.renorm) {
-        const double den = lane_value(sum_phases<1>(lane < k ? w : 0.0), 0);
-        w = den != 0.0 ? w / den : 0.0;        // every chosen score underflowed: weights 0
+        double den = lane < k ? w : 0.0;                   // k <= 8: the slots lie in the first row of 16 lanes
+        den = add_row_ror<1>(den);
+        den = add_row_ror<2>(den);
+        den = add_row_ror<4>(den);
+        den = first_lane(add_row_ror<8>(den));
+        w = den != 0.0 ? w / den : 0.0;                    // every chosen score underflowed: weights 0
     }
     weight = (float)(w * rule.scale);
 }
@@ -211,11 +215,12 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 template <int NT>
 struct TileLds {
-    double red[kSelWaves][kTileT][NT * 16];
+    double red[kSelWaves][NT][kTileT][16];
     float wsq[kSelWaves][NT * 16];
     float xsq[kSelWaves][kTileT];
     float logit[kTileT][64];
     unsigned long long redo[kTileT];
+    int any;                                         // some logit needs the integer path
     long long ered[kSelWaves][2];
     SelectLds sel[kSelWaves];
     int cnt[MOE_MAX_EXPERTS];
@@ -292,7 +297,7 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S.red[wave][q + 4 * r][NT * j + n] = acc[n][r];
+        for (int r = 0; r < 4; ++r) S.red[wave][n][q + 4 * r][j] = acc[n][r];
     xsq = sum_phases<16>(xsq);
 #pragma unroll
     for (int n = 0; n < NT; ++n) wsq[n] = sum_phases<16>(wsq[n]);
@@ -302,32 +307,37 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         for (int n = 0; n < NT; ++n) S.wsq[wave][NT * j + n] = wsq[n];
     }
     if (tid < kTileT) S.redo[tid] = 0ull;
+    if (tid == 0) S.any = 0;
     if (tid < MOE_MAX_EXPERTS) S.cnt[tid] = 0;
     __syncthreads();
     constexpr int OUT = kTileT * NT * 16;
 #pragma unroll
     for (int o0 = 0; o0 < OUT; o0 += kSelThreads) {
         const int o = o0 + tid;
-        const int tt = o / (NT * 16), e = o % (NT * 16);
+        const int n = o / (kTileT * 16), tt = o / 16 % kTileT, e = NT * (o % 16) + n;
         if (o >= OUT || e >= mine || t0 + tt >= T) continue;
         double v = 0.0;
         float X = 0.0f, W = 0.0f;
 #pragma unroll
         for (int w = 0; w < kSelWaves; ++w) {
-            v += S.red[w][tt][e];
+            v += S.red[w][n][tt][o % 16];
             X += S.xsq[w][tt];
             W += S.wsq[w][e];
         }
         // |v - exact| <= n 2^-53 (1 + n 2^-53) sum|x w| for paths of at most n additions, and
-        // sum|x w| <= sqrt(X W) with both FP32 sums of exact squares (at most H roundings,
-        // H <= 4096) within a factor 1 + 2^-11 of their true values.
-        const double err = (double)(H / kSelWaves + kSelWaves + 1) * 0x1p-53 * sqrt((double)X * (double)W) *
-                           (1.0 + 0x1p-9);
+        // sum|x w| <= sqrt(X W).  The FP32 sums of exact squares (at most H <= 4096 roundings) are
+        // within a factor 1 + 2^-11 of their true values, the root and the products below within
+        // 1 + 2^-20.
+        const float err = (float)(H / kSelWaves + kSelWaves + 1) * 0x1p-53f *
+                          (__builtin_amdgcn_sqrtf(X * W) * (1.0f + 0x1p-9f));
         S.logit[tt][e] = (float)v;
-        if (isfinite(v) && !rn32_certain(v, err)) atomicOr(&S.redo[tt], 1ull << e);
+        if (isfinite(v) && !rn32_certain(v, (double)err)) {
+            atomicOr(&S.redo[tt], 1ull << e);
+            S.any = 1;
+        }
     }
     __syncthreads();
-    for (int tt = 0; tt < kTileT; ++tt) {
+    for (int tt = 0; S.any && tt < kTileT; ++tt) {
         unsigned long long redo = S.redo[tt];
         while (redo) {                               // rare: exact recomputation by the whole block
             const int e = __builtin_ctzll(redo);
