@@ -37,7 +37,8 @@ struct ScoreRule {
 
 // LDS of one wavefront's selection.  A wavefront's LDS operations complete in
 // order, so its lanes exchange values through it without a barrier.
-struct SelectLds {
+typedef int Int4 __attribute__((ext_vector_type(4), may_alias));
+struct __attribute__((aligned(16))) SelectLds {
     double s[64], c[64];     // scores, choice values
     double top[2][64];       // a group's two largest choice values
     double value[64];        // group values
@@ -110,11 +111,11 @@ __device__ inline void select_wave(const ScoreRule &rule, int E, int k, int lane
     S.key[lane] = key;
     if (lane < MOE_MAX_TOPK) S.slot[lane] = 0;
     int rank = 0;
-    const int4 *keys = reinterpret_cast<const int4 *>(S.key);
+    const Int4 *keys = reinterpret_cast<const Int4 *>(S.key);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const int4 o = keys[i];
-        rank += (o.x > key ? 1 : 0) + (o.y > key ? 1 : 0) + (o.z > key ? 1 : 0) + (o.w > key ? 1 : 0);
+        const Int4 o = keys[i];
+        rank += (o[0] > key ? 1 : 0) + (o[1] > key ? 1 : 0) + (o[2] > key ? 1 : 0) + (o[3] > key ? 1 : 0);
     }
     const bool chosen = in && rank < k;
     if (chosen) S.slot[rank] = lane + 1;
