@@ -241,6 +241,21 @@ __device__ void topk_softmax_wave(const RouteArgs &a, const int (&tok)[NTOK], in
     }
 }
 
+// FP16 bits of a nonzero magnitude, less one; a zero gives the largest value,
+// so the minimum over a row is that of its nonzero values.
+__device__ inline uint32_t magnitude_less_one(uint32_t bits) { return (bits & 0x7fffu) - 1u; }
+
+// True when fp64 sums of the products of a row of FP16 activations, whose
+// smallest nonzero magnitude is min_less_one (magnitude_less_one), with any
+// FP16 weights are exact in every order: the activations are multiples of
+// 2^(q-25), q = max(exponent field, 1), the weights of 2^-24, and partial sums
+// below 2^(4+q) (bound: of sum |x w|) have at most 53 bits above 2^(q-49).
+__device__ inline bool sums_exact(uint32_t min_less_one, float bound)
+{
+    const uint32_t e = (min_less_one + 1u) >> 10;                // 0 also for a row of zeros
+    return bound < ldexpf(1.0f, 4 + (int)max(e, 1u));
+}
+
 // Loads VEC consecutive FP16 router weights (experts e0 .. e0+VEC-1 of row h).
 template <int VEC>
 struct WLoad;
@@ -416,12 +431,14 @@ struct LogitsLds {
     long long red[kSelWaves][2];
     float logit[kGroupE];
     unsigned long long redo;
+    uint32_t xmin[kSelWaves];
 };
 
 // DEV: the logits go to a.lbuf at device scope (read by another block of the
-// same launch).  NONFINITE: a sum that is infinite or NaN is the logit (the
-// integer path would read such inputs as numbers).
-template <int VEC, bool DEV = false, bool NONFINITE = false>
+// same launch).  SCORED (the routing by scores): a sum that is infinite or NaN
+// is the logit (the integer path would read such inputs as numbers), and rows
+// whose fp64 sums are exact need no error bound.
+template <int VEC, bool DEV = false, bool SCORED = false>
 __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
 {
     constexpr int EQ = kGroupE / VEC;
@@ -477,6 +494,20 @@ __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
                 for (int j = 0; j < 4; ++j) s_x[4 * i + j] = h2d((uint16_t)(v[r][j >> 1] >> (16 * (j & 1))));
             }
         }
+        if constexpr (SCORED) {
+            uint32_t m = ~0u;                          // the loads are clamped: repeated values change no minimum
+#pragma unroll
+            for (int r = 0; r < kMaxH / 4 / kSelThreads; ++r)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = min(m, magnitude_less_one(v[r][j >> 1] >> (16 * (j & 1))));
+            m = min(m, moe::ror_u32<1>(m));
+            m = min(m, moe::ror_u32<2>(m));
+            m = min(m, moe::ror_u32<4>(m));
+            m = min(m, moe::ror_u32<8>(m));
+            m = min(m, moe::partner_u32<true>(m));
+            m = min(m, moe::partner_u32<false>(m));
+            if (lane == 0) S.xmin[wave] = m;
+        }
     }
     __syncthreads();
 
@@ -529,8 +560,13 @@ __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
         // most n roundings) is within a factor 1 + 2^-16 of the true sum|x*w|.
         // Hence err = 2^(ceil(log2 n) + 1 - 53) * B covers it.
         const double err = ldexp((double)B, kErrExp);
-        const bool certain = lane >= kGroupE || e >= E || (NONFINITE && !isfinite(v)) ||
-                             (!a.force_exact && rn32_certain(v, err));
+        bool certain = lane >= kGroupE || e >= E || (!a.force_exact && rn32_certain(v, err));
+        if constexpr (SCORED) {
+            uint32_t m = ~0u;
+#pragma unroll
+            for (int r = 0; r < kSelWaves; ++r) m = min(m, S.xmin[r]);
+            certain = certain || !isfinite(v) || sums_exact(m, B * (1.0f + 0x1p-15f));
+        }
         if (lane < kGroupE) s_logit[lane] = (float)v;
         const unsigned long long m = __ballot(!certain);
         if (lane == 0) s_redo = m;

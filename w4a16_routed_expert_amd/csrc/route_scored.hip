@@ -208,8 +208,10 @@ __global__ __launch_bounds__(kSelThreads) void route_scored_small_kernel(RouteAr
 // j is expert NT*j + n; the columns are a permutation of the experts).  The
 // loads of a step are in flight while the one before it is multiplied.
 //   fp64 matrix instruction, 16x16x4: the products of FP16 values are exact in
-//   fp64; a wavefront's chain has H/8 additions per output and the 8 partial
-//   sums are added in order: at most H/8 + 8 additions on a path.
+//   fp64; a step sums 32 of them, a wavefront its H/256 steps, the block its 8
+//   wavefronts: at most 32 + H/256 + 1 + 8 additions on a path (short paths keep
+//   the error bound small, and with it the number of logits that need the
+//   integer path).
 constexpr int kTileT = 16;
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
@@ -219,10 +221,11 @@ struct TileLds {
     double red[kSelWaves][NT][kTileT][16];
     float wsq[kSelWaves][NT * 16];
     float xsq[kSelWaves][kTileT];
+    uint32_t xmin[kSelWaves][kTileT];
     float logit[kTileT][64];
     unsigned long long redo[kTileT];
     int any;                                         // some logit needs the integer path
-    long long ered[kSelWaves][2];
+    double ered[kSelWaves][2];
     SelectLds sel[kSelWaves];
     int cnt[MOE_MAX_EXPERTS];
     int last;
@@ -253,6 +256,64 @@ struct TileStep {
     __device__ inline uint16_t weight(int i, int n) const { return WIDE ? WLoad<NT>::get(w[i], n) : w1[i][WIDE ? 0 : n]; }
 };
 
+// s + c of a running sum after adding p: s the rounded sum, c the sum of the
+// additions' errors (each exact, by the error-free transformation of a sum).
+__device__ inline void add_exact(double &s, double &c, double p)
+{
+    const double t = s + p, z = t - s;
+    c += (s - (t - z)) + (p - z);
+    s = t;
+}
+
+// The correctly rounded logit of token t and expert e by the whole block, for
+// the rare sum near a rounding border.  Products and partial sums of FP16 x FP16
+// are multiples of 2^-48 below 2^44, so s holds their leading 53 bits and c (a
+// sum of multiples of 2^-48 below 2^5) the rest: s + c is the exact sum.  Rounding
+// hi + lo to odd before the rounding to FP32 makes that one correct rounding.
+// Few instructions: this code is seldom in the instruction cache, and a launch
+// waits for its slowest tile.  Valid in every thread.
+__device__ inline float exact_logit_block(const RouteArgs &a, int t, int e, double (*red)[2])
+{
+    const int tid = threadIdx.x;
+    double s = 0.0, c = 0.0;
+    const uint16_t *x = a.x + (size_t)t * a.H, *w = a.wr + e;
+#pragma unroll 1
+    for (int h0 = tid; h0 < a.H; h0 += 4 * kSelThreads) {              // four pairs of loads in flight
+        uint16_t xv[4], wv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int h = h0 + i * kSelThreads, hc = min(h, a.H - 1);
+            xv[i] = h < a.H ? x[hc] : (uint16_t)0;
+            wv[i] = w[(size_t)hc * a.E];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) add_exact(s, c, h2d(xv[i]) * h2d(wv[i]));
+    }
+#pragma unroll 1
+    for (int off = 32; off >= 1; off >>= 1) {
+        const double os = __shfl_xor(s, off);
+        c += __shfl_xor(c, off);
+        add_exact(s, c, os);
+    }
+    if ((tid & 63) == 0) {
+        red[tid >> 6][0] = s;
+        red[tid >> 6][1] = c;
+    }
+    __syncthreads();
+    s = red[0][0];
+    c = red[0][1];
+#pragma unroll 1
+    for (int i = 1; i < kSelWaves; ++i) {
+        c += red[i][1];
+        add_exact(s, c, red[i][0]);
+    }
+    __syncthreads();                                                   // red is reused by the next call
+    const double hi = s + c, lo = c - (hi - s);
+    uint64_t b = __builtin_bit_cast(uint64_t, hi);
+    if (lo != 0.0 && !(b & 1)) b += (lo > 0.0) == (hi > 0.0) ? 1 : -1;
+    return (float)__builtin_bit_cast(double, b);
+}
+
 // Grid: tiles x parts (part p: experts 16 NT p and on).  With more than one
 // part the logits meet in a.lbuf ([T][E], device scope) and done[tile] counts
 // the parts stored (zero before and after).  counts[tile][E]: the tile's pairs per expert.
@@ -267,11 +328,12 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
     const int first = blockIdx.y * (16 * NT), mine = min(E - first, 16 * NT);   // this block's experts
     const int j = lane & 15, q = lane >> 4;
 
-    f64x4 acc[NT];
+    f64x4 sum[NT];
     float wsq[NT], xsq = 0.0f;
+    uint32_t xmin = ~0u;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        acc[n] = f64x4{0.0, 0.0, 0.0, 0.0};
+        sum[n] = f64x4{0.0, 0.0, 0.0, 0.0};
         wsq[n] = 0.0f;
     }
     const uint16_t *xrow = a.x + (size_t)min(t0 + j, T - 1) * H + 8 * q;
@@ -281,10 +343,14 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
     if (32 * wave < H) cur.load(xrow, wcol, 32 * wave, E, mine - e0);
     for (int h0 = 32 * wave; h0 < H; h0 += 32 * kSelWaves) {
         if (h0 + 32 * kSelWaves < H) nxt.load(xrow, wcol, h0 + 32 * kSelWaves, E, mine - e0);
+        f64x4 acc[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[n] = f64x4{0.0, 0.0, 0.0, 0.0};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float xf = (float)__builtin_bit_cast(_Float16, WLoad<8>::get(cur.x, i));
             xsq = fmaf(xf, xf, xsq);
+            xmin = min(xmin, magnitude_less_one(WLoad<8>::get(cur.x, i)));
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float wf = (float)__builtin_bit_cast(_Float16, cur.weight(i, n));
@@ -292,18 +358,23 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
                 acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)xf, (double)wf, acc[n], 0, 0, 0);
             }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sum[n] += acc[n];
         cur = nxt;
     }
     // partial sums of this wavefront: lane (q, j) holds tokens q + 4r of column j
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S.red[wave][n][q + 4 * r][j] = acc[n][r];
+        for (int r = 0; r < 4; ++r) S.red[wave][n][q + 4 * r][j] = sum[n][r];
     xsq = sum_phases<16>(xsq);
+    xmin = min(xmin, moe::partner_u32<true>(xmin));
+    xmin = min(xmin, moe::partner_u32<false>(xmin));
 #pragma unroll
     for (int n = 0; n < NT; ++n) wsq[n] = sum_phases<16>(wsq[n]);
     if (q == 0) {
         S.xsq[wave][j] = xsq;
+        S.xmin[wave][j] = xmin;
 #pragma unroll
         for (int n = 0; n < NT; ++n) S.wsq[wave][NT * j + n] = wsq[n];
     }
@@ -319,9 +390,11 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         if (o >= OUT || e >= mine || t0 + tt >= T) continue;
         double v = 0.0;
         float X = 0.0f, W = 0.0f;
+        uint32_t least = ~0u;
 #pragma unroll
         for (int w = 0; w < kSelWaves; ++w) {
             v += S.red[w][n][tt][o % 16];
+            least = min(least, S.xmin[w][tt]);
             X += S.xsq[w][tt];
             W += S.wsq[w][e];
         }
@@ -329,10 +402,10 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         // sum|x w| <= sqrt(X W).  The FP32 sums of exact squares (at most H <= 4096 roundings) are
         // within a factor 1 + 2^-11 of their true values, the root and the products below within
         // 1 + 2^-20.
-        const float err = (float)(H / kSelWaves + kSelWaves + 1) * 0x1p-53f *
-                          (__builtin_amdgcn_sqrtf(X * W) * (1.0f + 0x1p-9f));
+        const float bound = __builtin_amdgcn_sqrtf(X * W) * (1.0f + 0x1p-9f);
+        const float err = (float)(32 + H / (32 * kSelWaves) + 1 + kSelWaves) * 0x1p-53f * bound;
         S.logit[tt][e] = (float)v;
-        if (isfinite(v) && !rn32_certain(v, (double)err)) {
+        if (isfinite(v) && !sums_exact(least, bound) && !rn32_certain(v, (double)err)) {
             atomicOr(&S.redo[tt], 1ull << e);
             S.any = 1;
         }
@@ -343,8 +416,7 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         while (redo) {                               // rare: exact recomputation by the whole block
             const int e = __builtin_ctzll(redo);
             redo &= redo - 1ull;
-            const float l = exact_logit(a, reinterpret_cast<const _Float16 *>(a.x) + (size_t)(t0 + tt) * H, first + e,
-                                        S.ered);
+            const float l = exact_logit_block(a, t0 + tt, first + e, S.ered);
             if (tid == 0) S.logit[tt][e] = l;
         }
     }
