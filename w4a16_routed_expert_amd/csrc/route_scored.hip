@@ -201,32 +201,37 @@ __global__ __launch_bounds__(kSelThreads) void route_scored_small_kernel(RouteAr
 }
 
 // ------------------------------------------------------------ larger batches
-// Block: 16 tokens x 16 NT experts.  Its 8 wavefronts split H; a wavefront's step
+// Block: 16 tokens x 16 NT experts.  Its 16 wavefronts split H; a wavefront's step
 // takes 32 values of H: lane 16q + j holds 8 of token j (values 8q .. 8q + 7 of
 // the step) and, per value, the NT experts NT*j .. NT*j + NT - 1 of that router
 // row, so one load of NT experts feeds NT matrix instructions (tile n's column
 // j is expert NT*j + n; the columns are a permutation of the experts).  The
 // loads of a step are in flight while the one before it is multiplied.
 //   fp64 matrix instruction, 16x16x4: the products of FP16 values are exact in
-//   fp64; a step sums 32 of them, a wavefront its H/256 steps, the block its 8
-//   wavefronts: at most 32 + H/256 + 1 + 8 additions on a path (short paths keep
-//   the error bound small, and with it the number of logits that need the
-//   integer path).
+//   fp64; a wavefront's chain has H/16 additions per output and the 16 partial
+//   sums are added in order: at most H/16 + 16 additions on a path.
+// 16 wavefronts: the instruction's unit is shared with the conversions to fp64,
+// which four wavefronts a SIMD overlap better than two, and each then selects
+// for one token.
 constexpr int kTileT = 16;
+constexpr int kTileThreads = 1024;
+constexpr int kTileWaves = kTileThreads / 64;
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 template <int NT>
 struct TileLds {
-    double red[kSelWaves][NT][kTileT][16];
-    float wsq[kSelWaves][NT * 16];
-    float xsq[kSelWaves][kTileT];
-    uint32_t xmin[kSelWaves][kTileT];
+    union {
+        double red[kTileWaves][NT][kTileT][16];
+        SelectLds sel[kTileWaves];               // once the sums are taken
+    };
+    float wsq[kTileWaves][NT * 16];
+    float xsq[kTileWaves][kTileT];
+    uint32_t xmin[kTileWaves][kTileT];
     float logit[kTileT][64];
     unsigned long long redo[kTileT];
     int any;                                         // some logit needs the integer path
-    double ered[kSelWaves][2];
-    SelectLds sel[kSelWaves];
+    double ered[kTileWaves][2];
     int cnt[MOE_MAX_EXPERTS];
     int last;
 };
@@ -278,11 +283,11 @@ __device__ inline float exact_logit_block(const RouteArgs &a, int t, int e, doub
     double s = 0.0, c = 0.0;
     const uint16_t *x = a.x + (size_t)t * a.H, *w = a.wr + e;
 #pragma unroll 1
-    for (int h0 = tid; h0 < a.H; h0 += 4 * kSelThreads) {              // four pairs of loads in flight
+    for (int h0 = tid; h0 < a.H; h0 += 4 * kTileThreads) {              // four pairs of loads in flight
         uint16_t xv[4], wv[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int h = h0 + i * kSelThreads, hc = min(h, a.H - 1);
+            const int h = h0 + i * kTileThreads, hc = min(h, a.H - 1);
             xv[i] = h < a.H ? x[hc] : (uint16_t)0;
             wv[i] = w[(size_t)hc * a.E];
         }
@@ -303,7 +308,7 @@ __device__ inline float exact_logit_block(const RouteArgs &a, int t, int e, doub
     s = red[0][0];
     c = red[0][1];
 #pragma unroll 1
-    for (int i = 1; i < kSelWaves; ++i) {
+    for (int i = 1; i < kTileWaves; ++i) {
         c += red[i][1];
         add_exact(s, c, red[i][0]);
     }
@@ -318,7 +323,7 @@ __device__ inline float exact_logit_block(const RouteArgs &a, int t, int e, doub
 // part the logits meet in a.lbuf ([T][E], device scope) and done[tile] counts
 // the parts stored (zero before and after).  counts[tile][E]: the tile's pairs per expert.
 template <int NT, bool WIDE>
-__global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, ScoreRule rule, int *counts,
+__global__ __launch_bounds__(kTileThreads) void route_tile_kernel(RouteArgs a, ScoreRule rule, int *counts,
                                                                  unsigned int *done)
 {
     __shared__ TileLds<NT> S;
@@ -328,24 +333,23 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
     const int first = blockIdx.y * (16 * NT), mine = min(E - first, 16 * NT);   // this block's experts
     const int j = lane & 15, q = lane >> 4;
 
-    f64x4 sum[NT];
+    f64x4 acc[NT];
     float wsq[NT], xsq = 0.0f;
     uint32_t xmin = ~0u;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        sum[n] = f64x4{0.0, 0.0, 0.0, 0.0};
+        acc[n] = f64x4{0.0, 0.0, 0.0, 0.0};
         wsq[n] = 0.0f;
     }
     const uint16_t *xrow = a.x + (size_t)min(t0 + j, T - 1) * H + 8 * q;
     const int e0 = NT * j < mine ? NT * j : 0;       // lanes past the experts repeat the first (their columns are not read)
     const uint16_t *wcol = a.wr + (size_t)(8 * q) * E + first + e0;
+    // single router loads (an odd number of experts, or an unaligned router) leave no registers for a second step
     TileStep<NT, WIDE> cur, nxt;
-    if (32 * wave < H) cur.load(xrow, wcol, 32 * wave, E, mine - e0);
-    for (int h0 = 32 * wave; h0 < H; h0 += 32 * kSelWaves) {
-        if (h0 + 32 * kSelWaves < H) nxt.load(xrow, wcol, h0 + 32 * kSelWaves, E, mine - e0);
-        f64x4 acc[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[n] = f64x4{0.0, 0.0, 0.0, 0.0};
+    if (WIDE && 32 * wave < H) cur.load(xrow, wcol, 32 * wave, E, mine - e0);
+    for (int h0 = 32 * wave; h0 < H; h0 += 32 * kTileWaves) {
+        if (!WIDE) cur.load(xrow, wcol, h0, E, mine - e0);
+        else if (h0 + 32 * kTileWaves < H) nxt.load(xrow, wcol, h0 + 32 * kTileWaves, E, mine - e0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float xf = (float)__builtin_bit_cast(_Float16, WLoad<8>::get(cur.x, i));
@@ -358,15 +362,13 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
                 acc[n] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)xf, (double)wf, acc[n], 0, 0, 0);
             }
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sum[n] += acc[n];
-        cur = nxt;
+        if (WIDE) cur = nxt;
     }
     // partial sums of this wavefront: lane (q, j) holds tokens q + 4r of column j
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) S.red[wave][n][q + 4 * r][j] = sum[n][r];
+        for (int r = 0; r < 4; ++r) S.red[wave][n][q + 4 * r][j] = acc[n][r];
     xsq = sum_phases<16>(xsq);
     xmin = min(xmin, moe::partner_u32<true>(xmin));
     xmin = min(xmin, moe::partner_u32<false>(xmin));
@@ -384,7 +386,7 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
     __syncthreads();
     constexpr int OUT = kTileT * NT * 16;
 #pragma unroll
-    for (int o0 = 0; o0 < OUT; o0 += kSelThreads) {
+    for (int o0 = 0; o0 < OUT; o0 += kTileThreads) {
         const int o = o0 + tid;
         const int n = o / (kTileT * 16), tt = o / 16 % kTileT, e = NT * (o % 16) + n;
         if (o >= OUT || e >= mine || t0 + tt >= T) continue;
@@ -392,7 +394,7 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         float X = 0.0f, W = 0.0f;
         uint32_t least = ~0u;
 #pragma unroll
-        for (int w = 0; w < kSelWaves; ++w) {
+        for (int w = 0; w < kTileWaves; ++w) {
             v += S.red[w][n][tt][o % 16];
             least = min(least, S.xmin[w][tt]);
             X += S.xsq[w][tt];
@@ -403,7 +405,7 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         // within a factor 1 + 2^-11 of their true values, the root and the products below within
         // 1 + 2^-20.
         const float bound = __builtin_amdgcn_sqrtf(X * W) * (1.0f + 0x1p-9f);
-        const float err = (float)(32 + H / (32 * kSelWaves) + 1 + kSelWaves) * 0x1p-53f * bound;
+        const float err = (float)(H / kTileWaves + 32 + kTileWaves) * 0x1p-53f * bound;
         S.logit[tt][e] = (float)v;
         if (isfinite(v) && !sums_exact(least, bound) && !rn32_certain(v, (double)err)) {
             atomicOr(&S.redo[tt], 1ull << e);
@@ -422,7 +424,7 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
     }
     __syncthreads();
     if (gridDim.y > 1) {
-        for (int o = tid; o < OUT; o += kSelThreads) {
+        for (int o = tid; o < OUT; o += kTileThreads) {
             const int tt = o / (NT * 16), e = o % (NT * 16);
             if (e < mine && t0 + tt < T) moe::store_dev(&a.lbuf[(size_t)(t0 + tt) * E + first + e], S.logit[tt][e]);
         }
@@ -437,9 +439,8 @@ __global__ __launch_bounds__(kSelThreads) void route_tile_kernel(RouteArgs a, Sc
         __syncthreads();
         if (!S.last) return;
     }
-    for (int tt = wave; tt < kTileT; tt += kSelWaves) {
-        const int t = t0 + tt;
-        if (t >= T) break;
+    const int tt = wave, t = t0 + tt;
+    if (t < T) {
         const int e = min(lane, E - 1);
         const float lv = gridDim.y > 1 ? moe::load_dev(&a.lbuf[(size_t)t * E + e]) : S.logit[tt][e];
         if (a.logits && lane < E) a.logits[(size_t)t * E + lane] = lv;
@@ -541,6 +542,7 @@ constexpr int kSplitTiles = 128;
 // Workspace: the counters (zero between calls), then the logits handed between
 // blocks, then the tiles' counts.
 constexpr size_t kScoredCtrl = 1024;
+static_assert(kTileWaves == kTileT, "one wavefront selects for one token");
 static_assert(kScoredCtrl >= (kScoredSmallT + 1) * sizeof(int) && kScoredCtrl >= kSplitTiles * sizeof(int), "counters");
 
 size_t scored_lbuf_bytes(int T, int E)
@@ -560,8 +562,8 @@ void launch_tiles(const RouteArgs &a, const ScoreRule &rule, int *counts, unsign
 {
     const dim3 grid((unsigned int)((a.T + kTileT - 1) / kTileT), (unsigned int)((a.E + 16 * NT - 1) / (16 * NT)));
     if (a.E % NT == 0 && moe::aligned(a.wr, 2 * NT))
-        hipLaunchKernelGGL((route_tile_kernel<NT, true>), grid, dim3(kSelThreads), 0, s, a, rule, counts, done);
-    else hipLaunchKernelGGL((route_tile_kernel<NT, false>), grid, dim3(kSelThreads), 0, s, a, rule, counts, done);
+        hipLaunchKernelGGL((route_tile_kernel<NT, true>), grid, dim3(kTileThreads), 0, s, a, rule, counts, done);
+    else hipLaunchKernelGGL((route_tile_kernel<NT, false>), grid, dim3(kTileThreads), 0, s, a, rule, counts, done);
 }
 
 }  // namespace
