@@ -437,11 +437,11 @@ struct LogitsLds {
 // DEV: the logits go to a.lbuf at device scope (read by another block of the
 // same launch).  SCORED (the routing by scores): a sum that is infinite or NaN
 // is the logit (the integer path would read such inputs as numbers), and rows
-// whose fp64 sums are exact need no error bound.
-template <int VEC, bool DEV = false, bool SCORED = false>
+// whose fp64 sums are exact need no error bound.  GE: experts of the block.
+template <int VEC, bool DEV = false, bool SCORED = false, int GE = kGroupE>
 __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
 {
-    constexpr int EQ = kGroupE / VEC;
+    constexpr int EQ = GE / VEC;
     constexpr int RPW = 64 / EQ;
     // rows in flight per thread: 16 (two batches for H = 2048; 32 in one
     // batch measured no faster and needs 152 VGPRs instead of 96, too many
@@ -461,7 +461,7 @@ __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
     unsigned long long &s_redo = S.redo;
 
     const int eq = lane % EQ, hp = lane / EQ;
-    const int e0 = g * kGroupE + VEC * eq;          // first expert of this lane
+    const int e0 = g * GE + VEC * eq;          // first expert of this lane
     const uint16_t *wcol = a.wr + (e0 < E ? e0 : 0);
     const int step = RPW * kSelWaves;
     int h0 = RPW * wave + hp;
@@ -545,10 +545,10 @@ __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
     }
     __syncthreads();
     if (wave == 0) {
-        const int e = g * kGroupE + lane;
+        const int e = g * GE + lane;
         double v = 0.0;
         float B = 0.0f;
-        if (lane < kGroupE) {
+        if (lane < GE) {
             for (int r = 0; r < kSelWaves; ++r) {
                 v += s_acc[r][lane];
                 B += s_bnd[r][lane];
@@ -560,14 +560,14 @@ __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
         // most n roundings) is within a factor 1 + 2^-16 of the true sum|x*w|.
         // Hence err = 2^(ceil(log2 n) + 1 - 53) * B covers it.
         const double err = ldexp((double)B, kErrExp);
-        bool certain = lane >= kGroupE || e >= E || (!a.force_exact && rn32_certain(v, err));
+        bool certain = lane >= GE || e >= E || (!a.force_exact && rn32_certain(v, err));
         if constexpr (SCORED) {
             uint32_t m = ~0u;
 #pragma unroll
             for (int r = 0; r < kSelWaves; ++r) m = min(m, S.xmin[r]);
             certain = certain || !isfinite(v) || sums_exact(m, B * (1.0f + 0x1p-15f));
         }
-        if (lane < kGroupE) s_logit[lane] = (float)v;
+        if (lane < GE) s_logit[lane] = (float)v;
         const unsigned long long m = __ballot(!certain);
         if (lane == 0) s_redo = m;
     }
@@ -576,12 +576,12 @@ __device__ void logits_block(const RouteArgs &a, LogitsLds &S, int t, int g)
     while (redo) {                                   // rare: exact recomputation by the whole block
         const int j = __builtin_ctzll(redo);
         redo &= redo - 1ull;
-        const float l = exact_logit(a, s_x, g * kGroupE + j, s_red);
+        const float l = exact_logit(a, s_x, g * GE + j, s_red);
         if (tid == 0) s_logit[j] = l;
     }
     __syncthreads();
-    if (tid < kGroupE) {
-        const int e = g * kGroupE + tid;
+    if (tid < GE) {
+        const int e = g * GE + tid;
         if (e < E) {
             float lv = s_logit[tid];
             if (a.bias) lv = lv + a.bias[e];

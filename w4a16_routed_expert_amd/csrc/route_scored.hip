@@ -146,13 +146,50 @@ __device__ inline void select_wave(const ScoreRule &rule, int E, int k, int lane
 // ------------------------------------------------------------ small batches: one launch
 constexpr int kScoredSmallT = 64;            // largest batch routed in one launch
 
+constexpr int kSmallE = 8;                   // experts per block of its logits
+
 union SmallLds {
     LogitsLds lg;
-    struct {
-        GroupLds<kSelWaves, true> gr;
-        SelectLds sel;
-    } g;
+    SelectLds sel;
+    int cnt[kSelWaves][MOE_MAX_EXPERTS];
 };
+
+// moe_route's grouping of a small batch whose pair p has expert e in lane p % 64
+// of wavefront p / 64 (e < 0: no pair); `waves` wavefronts hold pairs.  A pair's
+// rank among the equal experts of its wavefront comes from ballots; the
+// wavefronts' counts, exchanged through LDS once, give each its start per expert.
+__device__ inline void group_small(const RouteArgs &a, int e, int waves, int (*cnt)[MOE_MAX_EXPERTS])
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const unsigned long long below = (1ull << lane) - 1ull, peers = same_expert_lanes(e);
+    const int rank = __popcll(peers & below);
+    cnt[wave][lane] = 0;
+    if (e >= 0 && rank == 0) cnt[wave][e] = __popcll(peers);
+    if (waves > 1) __syncthreads();
+    int total = 0, before = 0;                   // of expert `lane`: all pairs, those of earlier wavefronts
+    for (int w = 0; w < waves; ++w) {
+        const int c = cnt[w][lane];
+        total += c;
+        before += w < wave ? c : 0;
+    }
+    const int incl = moe::wave_inclusive_sum(total), start = incl - total + before;
+    if (wave == 0) {
+        const unsigned long long act = __ballot(total > 0);
+        const int na = __popcll(act);
+        if (lane < a.E) {
+            a.offsets[lane] = incl - total;
+            if (total > 0) a.active[__popcll(act & below)] = lane;
+            if (lane >= na) a.active[lane] = -1;
+            if (lane == a.E - 1) a.offsets[a.E] = incl;
+        }
+        if (lane == 0) a.n_active[0] = na;
+    }
+    const int pos = __builtin_amdgcn_ds_bpermute(4 * max(e, 0), start) + rank;
+    if (e >= 0) {
+        a.sorted_pairs[pos] = (int)threadIdx.x;
+        a.pair_pos[threadIdx.x] = pos;
+    }
+}
 
 // done[t]: blocks that have stored their logits of token t; done[kScoredSmallT]:
 // tokens selected.  All zero before and after the call.
@@ -160,11 +197,12 @@ template <int VEC>
 __global__ __launch_bounds__(kSelThreads) void route_scored_small_kernel(RouteArgs a, ScoreRule rule,
                                                                          unsigned int *done)
 {
+    static_assert(kScoredSmallT * MOE_MAX_TOPK <= kSelThreads, "one thread a pair");
     __shared__ SmallLds S;
     __shared__ int s_last, s_all;
-    const int G = (a.E + kGroupE - 1) / kGroupE;
+    const int G = (a.E + kSmallE - 1) / kSmallE;
     const int t = blockIdx.x / G, lane = threadIdx.x & 63;
-    logits_block<VEC, true, true>(a, S.lg, t, blockIdx.x % G);
+    logits_block<VEC, true, true, kSmallE>(a, S.lg, t, blockIdx.x % G);
     moe::wait_stores();                                     // this wave's logits are complete
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -177,27 +215,30 @@ __global__ __launch_bounds__(kSelThreads) void route_scored_small_kernel(RouteAr
         const float lv = moe::load_dev(a.lbuf + (size_t)t * a.E + min(lane, a.E - 1));
         int id;
         float w;
-        select_wave(rule, a.E, a.k, lane, lv, S.g.sel, id, w);
+        select_wave(rule, a.E, a.k, lane, lv, S.sel, id, w);
         if (a.logits && lane < a.E) a.logits[(size_t)t * a.E + lane] = lv;
         if (lane < a.k) {
             moe::store_dev(&a.ids[(size_t)t * a.k + lane], (int32_t)id);
             a.w[(size_t)t * a.k + lane] = w;
         }
-        moe::wait_stores();                                 // the ids are complete
-        if (lane == 0) {
-            done[t] = 0u;
-            unsigned int *all = done + kScoredSmallT;
-            const unsigned int before =
-                a.T == 1 ? 0u : __hip_atomic_fetch_add(all, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            s_all = before == (unsigned int)a.T - 1;
-            if (s_all && a.T > 1) *all = 0u;
+        if (lane == 0) done[t] = 0u;
+        if (a.T == 1) {                                     // the whole batch is in this wavefront
+            group_small(a, lane < a.k ? id : -1, 1, S.cnt);
+        } else {
+            moe::wait_stores();                             // the ids are complete
+            if (lane == 0) {
+                unsigned int *all = done + kScoredSmallT;
+                const unsigned int before = __hip_atomic_fetch_add(all, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                s_all = before == (unsigned int)a.T - 1;
+                if (s_all) *all = 0u;
+            }
         }
     }
+    if (a.T == 1) return;
     __syncthreads();
     if (!s_all) return;
-    for (int p = threadIdx.x; p < a.T * a.k; p += kSelThreads) S.g.gr.ids[p] = moe::load_dev(&a.ids[p]);
-    __syncthreads();
-    group_sort<kSelWaves, true, false>(a, S.g.gr);
+    const int p = threadIdx.x;
+    group_small(a, p < a.T * a.k ? moe::load_dev(&a.ids[p]) : -1, (a.T * a.k + 63) / 64, S.cnt);
 }
 
 // ------------------------------------------------------------ larger batches
@@ -640,7 +681,7 @@ int moe_route_scored(const void *x_dev, const void *w_router_dev, const float *s
     hipStream_t s = (hipStream_t)stream;
     if (T <= kScoredSmallT) {
         unsigned int *done = (unsigned int *)ws_dev;
-        const unsigned int blocks = (unsigned int)T * (unsigned int)((E + kGroupE - 1) / kGroupE);
+        const unsigned int blocks = (unsigned int)T * (unsigned int)((E + kSmallE - 1) / kSmallE);
         if (E % 2 == 0 && moe::aligned(w_router_dev, 4))
             hipLaunchKernelGGL(route_scored_small_kernel<2>, dim3(blocks), dim3(kSelThreads), 0, s, a, r, done);
         else hipLaunchKernelGGL(route_scored_small_kernel<1>, dim3(blocks), dim3(kSelThreads), 0, s, a, r, done);
