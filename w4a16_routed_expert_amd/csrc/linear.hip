@@ -215,6 +215,17 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
     f32x4 acc[FT];
 #pragma unroll
     for (int f = 0; f < FT; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // the epilogue's operands first: they arrive while the products are made.
+    // Two lanes a token: outputs 8h .. 8h + 7 are the results of lanes (2h, r) and (2h + 1, r)
+    const int et = t0 + (tid >> 1), eh = tid & 1;
+    Columns<E4M3> cols;
+    half8 res = {};
+    float sx = 1.0f;
+    if (tid < 32 * FT) {
+        cols.load(a, n0 + 8 * eh);
+        res = cols.residual(a, et);
+        if constexpr (E4M3) sx = a.x_scale[min(et, a.T - 1)];
+    }
     const bool real_w = n0 + r < a.N;
     for (int s = wave; 8 * s < a.chunks; s += NW * U) {
         i32x4 w[U][2], x[U][FT][2];
@@ -247,20 +258,15 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 #pragma unroll
     for (int f = 0; f < FT; ++f) s_acc[wave][f][lane] = acc[f];
     __syncthreads();
-    // two lanes a token: outputs 8h .. 8h + 7 are the results of lanes (2h, r) and (2h + 1, r)
     if (tid < 32 * FT) {
-        const int t = tid >> 1, h = tid & 1;
-        const int f = t >> 4, at = 32 * h + (t & 15);
-        Columns<E4M3> cols;
-        cols.load(a, n0 + 8 * h);
+        const int t = tid >> 1, f = t >> 4, at = 32 * eh + (t & 15);
         f32x4 lo = s_acc[0][f][at], hi = s_acc[0][f][at + 16];
 #pragma unroll
         for (int w = 1; w < NW; ++w) {
             lo += s_acc[w][f][at];
             hi += s_acc[w][f][at + 16];
         }
-        const half8 res = cols.residual(a, t0 + t);
-        cols.finish(a, t0 + t, lo, hi, E4M3 ? a.x_scale[min(t0 + t, a.T - 1)] : 1.0f, res);
+        cols.finish(a, et, lo, hi, sx, res);
     }
 }
 
