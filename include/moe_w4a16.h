@@ -405,8 +405,10 @@ int moe_shared_ffn(const void *x_dev, const void *w_gate_dev, const void *w_up_d
  * Limits: 0 <= T <= 65536, 1 <= N <= 2^24, 16 <= K <= 2^20 and a multiple of 16,
  *   ldx, ldw <= 2^22; rows of x and W start at multiples of 16 bytes; y and
  *   residual rows need 2-byte alignment (8 is faster).
- * ws_dev / ws_bytes: moe_linear_workspace_size(T, N, K, type) bytes, 256-byte
- *   aligned, no initialization; not shared by calls that can overlap. */
+ * ws_dev / ws_bytes: moe_linear_workspace_size(T, N, K, type) bytes (at most
+ *   32 MiB and 256 bytes), 256-byte aligned, no initialization; one sized for T
+ *   serves any T' <= T; not shared by calls that can overlap.
+ * One launch on `stream`, or two where k is divided among blocks. */
 enum moe_linear_type { MOE_LINEAR_FP16 = 0, MOE_LINEAR_E4M3 = 1 };
 enum moe_activation { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3 };
 size_t moe_linear_workspace_size(int T, int N, int K, int type);

@@ -117,7 +117,8 @@ class Case:
 SHAPES = [(1, 1, 16), (1, 2048, 2048), (2, 17, 32), (3, 100, 48), (15, 16, 64), (16, 63, 128), (17, 65, 144),
           (31, 250, 1040), (32, 64, 4096), (33, 129, 2064), (48, 1411, 80), (63, 30, 112), (64, 257, 512),
           (65, 64, 16), (65, 1, 2048), (100, 333, 272), (127, 129, 1424), (129, 70, 64), (200, 640, 96), (256, 256, 8192),
-          (333, 1411, 176), (700, 515, 208), (1900, 1921, 80), (2049, 1700, 64), (4000, 3700, 144)]
+          (333, 1411, 176), (700, 515, 208), (1900, 1921, 80), (2049, 1700, 64), (4000, 3700, 144), (2700, 2000, 96),
+          (33, 70, 16384), (130, 90, 16400), (17, 300, 24576)]
 
 
 @pytest.mark.parametrize("type", [FP16, E4M3], ids=["fp16", "e4m3"])
@@ -205,7 +206,7 @@ def test_empty_batch_and_rows_past_2_gib():
     assert np.array_equal(y.cpu().numpy().astype(np.float64), x.astype(np.float64) @ w.astype(np.float64).T)
 
 
-@pytest.mark.parametrize("T,N,K", [(4, 640, 1024), (90, 200, 2048), (300, 300, 512)])
+@pytest.mark.parametrize("T,N,K", [(4, 640, 1024), (90, 200, 2048), (300, 300, 512), (40, 130, 8192), (1100, 900, 512)])
 def test_captured_replays_and_repeated_calls(T, N, K):
     from w4a16_routed_expert_amd import binding as B
     c = Case(T, N, K, FP16, whole=False)

@@ -9,7 +9,9 @@
 // instruction and the tokens its columns: a lane's four results are four
 // consecutive outputs n of one token.
 //   linear_stream_kernel: few tokens, bound by reading W once from HBM;
-//   linear_tile_kernel: many tokens, bound by the matrix cores and LDS.
+//   linear_tile_kernel: many tokens, bound by the matrix cores and LDS; where
+//   its tiles are too few for the GPU, k is divided among blocks and
+//   linear_join_kernel adds the splits in their order.
 #include "moe_internal.h"
 
 namespace {
@@ -32,6 +34,9 @@ struct LinearArgs {
     long long ldy;
     int T, N, chunks;                    // chunks: 16-byte chunks of a row
     int act;
+    float *planes;                       // [splits][T][plane_ld] partial sums, or null: k is not divided
+    int plane_ld;                        // N rounded up to 8
+    int split_steps;                     // 128-byte steps of k per split
 };
 
 // Rows of y and of the residual may start at any element: 16-byte accesses
@@ -95,6 +100,15 @@ struct Columns {
             h[r] = f;
         }
         return h;
+    }
+
+    // The 8 sums of token t as they are, to split `split`'s plane.
+    __device__ inline void store_plane(const LinearArgs &a, int split, int t, f32x4 lo, f32x4 hi) const
+    {
+        if (t >= a.T || m <= 0) return;
+        f32x4 *o = reinterpret_cast<f32x4 *>(a.planes + ((long long)split * a.T + t) * a.plane_ld + n);
+        o[0] = lo;
+        o[1] = hi;
     }
 
     // The 8 outputs of token t from their sums (lo, hi), the token's scale and
@@ -193,78 +207,67 @@ __device__ inline __amdgpu_buffer_rsrc_t rows_rsrc(const uint8_t *base, long lon
 // load returns zeros.
 constexpr uint32_t kOutside = 0xC0000000u;
 
-// ------------------------------------------------------------ few tokens
-// Block: 16 rows of W, FT x 16 tokens, all of k; wavefront w takes the 128-byte
-// steps w, w + NW, ... and the NW partial sums meet in LDS.  Every lane asks
-// for U steps of W before it uses the first.
-template <bool E4M3, int FT, int NW>
+// ------------------------------------------------------------ at most 16 tokens
+// Block: 16 rows of W, all of k; wavefront w takes the 128-byte steps w, w + NW,
+// ... and the NW partial sums meet in LDS.  Every lane asks for U steps of both
+// operands before it uses the first.
+constexpr int kStreamT = 16;
+
+template <bool E4M3, int NW>
 __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 {
     typedef Step<E4M3, 16> S;
-    constexpr int U = FT >= 4 ? 2 : 4;
+    constexpr int U = 4;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int g = lane >> 4, r = lane & 15;
-    const int n0 = blockIdx.x * 16, t0 = blockIdx.y * (16 * FT);
-    __shared__ f32x4 s_acc[NW][FT][64];
+    const int n0 = blockIdx.x * 16;
+    __shared__ f32x4 s_acc[NW][64];
     const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + n0 * a.ldw, a.ldw, min(16, a.N - n0), a.chunks);
-    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + t0 * a.ldx, a.ldx, min(16 * FT, a.T - t0), a.chunks);
-    const uint32_t row_w = (uint32_t)(r * a.ldw);
-    uint32_t row_x[FT];
-#pragma unroll
-    for (int f = 0; f < FT; ++f) row_x[f] = t0 + 16 * f + r < a.T ? (uint32_t)((16 * f + r) * a.ldx) : kOutside;
-    f32x4 acc[FT];
-#pragma unroll
-    for (int f = 0; f < FT; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, a.ldx, a.T, a.chunks);
+    const uint32_t row_w = n0 + r < a.N ? (uint32_t)(r * a.ldw) : kOutside;
+    const uint32_t row_x = r < a.T ? (uint32_t)(r * a.ldx) : kOutside;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     // the epilogue's operands first: they arrive while the products are made.
     // Two lanes a token: outputs 8h .. 8h + 7 are the results of lanes (2h, r) and (2h + 1, r)
-    const int et = t0 + (tid >> 1), eh = tid & 1;
+    const int et = tid >> 1, eh = tid & 1;
     Columns<E4M3> cols;
     half8 res = {};
     float sx = 1.0f;
-    if (tid < 32 * FT) {
+    if (tid < 2 * kStreamT) {
         cols.load(a, n0 + 8 * eh);
         res = cols.residual(a, et);
         if constexpr (E4M3) sx = a.x_scale[min(et, a.T - 1)];
     }
-    const bool real_w = n0 + r < a.N;
     for (int s = wave; 8 * s < a.chunks; s += NW * U) {
-        i32x4 w[U][2], x[U][FT][2];
+        i32x4 w[U][2], x[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int c = 8 * (s + u * NW) + 4 * h + g;
-                const bool in = c < a.chunks;
-                w[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, in && real_w ? row_w + 16u * c : kOutside, 0, 0);
+                w[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, c < a.chunks ? row_w + 16u * c : kOutside, 0, 0);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int f = 0; f < FT; ++f)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int c = 8 * (s + u * NW) + 4 * h + g;
-                    const bool in = c < a.chunks && row_x[f] != kOutside;
-                    x[u][f][h] = __builtin_amdgcn_raw_buffer_load_b128(rx, in ? row_x[f] + 16u * c : kOutside, 0, 0);
-                }
+            for (int h = 0; h < 2; ++h) {
+                const int c = 8 * (s + u * NW) + 4 * h + g;
+                x[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rx, c < a.chunks ? row_x + 16u * c : kOutside, 0, 0);
+            }
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int f = 0; f < FT; ++f)
-#pragma unroll
-                for (int h = 0; h < S::kParts; ++h)
-                    acc[f] = S::mma(S::pick(w[u], h), S::pick(x[u][f], h), acc[f]);
+            for (int h = 0; h < S::kParts; ++h) acc = S::mma(S::pick(w[u], h), S::pick(x[u], h), acc);
     }
-#pragma unroll
-    for (int f = 0; f < FT; ++f) s_acc[wave][f][lane] = acc[f];
+    s_acc[wave][lane] = acc;
     __syncthreads();
-    if (tid < 32 * FT) {
-        const int t = tid >> 1, f = t >> 4, at = 32 * eh + (t & 15);
-        f32x4 lo = s_acc[0][f][at], hi = s_acc[0][f][at + 16];
+    if (tid < 2 * kStreamT) {
+        const int at = 32 * eh + et;
+        f32x4 lo = s_acc[0][at], hi = s_acc[0][at + 16];
 #pragma unroll
         for (int w = 1; w < NW; ++w) {
-            lo += s_acc[w][f][at];
-            hi += s_acc[w][f][at + 16];
+            lo += s_acc[w][at];
+            hi += s_acc[w][at + 16];
         }
         cols.finish(a, et, lo, hi, sx, res);
     }
@@ -272,7 +275,8 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 
 // ------------------------------------------------------------ many tokens
 // Block tile BN outputs x BT tokens by 4 wavefronts, 2 x 2, each BN/2 x BT/2 in
-// registers; 128 bytes of k a step.  A step's operands lie in LDS in three
+// registers (or KG such groups of 4, each taking every KG-th step of k, whose
+// sums meet in LDS: for tiles too few to fill the GPU); 128 bytes of k a step.  A step's operands lie in LDS in three
 // parts: the tokens X, and the first and second half (WA, WB) of every
 // wavefront's output rows, for B steps at once.  Per step:
 //     barrier; ask for WB of step k + B - 1; read WB(k); multiply WA(k) . X(k)
@@ -295,10 +299,10 @@ __device__ inline void arrive()
 
 // The parts of stage `STAGE` (0 X, 1 WA, 2 WB), each an LDS array of its own:
 // the compiler then knows which loads a read of LDS depends on.
-template <bool E4M3, int BN, int BT, int MT, int STAGE, int WHICH>
+template <bool E4M3, int BN, int BT, int MT, int KG, int STAGE, int WHICH>
 __device__ inline i32x4 *part()
 {
-    static __shared__ i32x4 s[WHICH == 0 ? BT * 8 : BN * 4];
+    static __shared__ i32x4 s[KG * (WHICH == 0 ? BT * 8 : BN * 4)];
     return s;
 }
 
@@ -307,7 +311,7 @@ struct Const {
     static constexpr int value = V;
 };
 
-template <bool E4M3, int BN, int BT, int MT, int B>
+template <bool E4M3, int BN, int BT, int MT, int B, int KG>
 __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t)
 {
     typedef Step<E4M3, MT> S;
@@ -315,7 +319,8 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     constexpr int FT = BT / 2 / MT, HN = BN / 4 / MT;            // MT x MT tiles of a wavefront: along t; along half its n
     constexpr int LX = BT / 32, LW = BN / 64;                    // loads (8 rows) of X and of a half of W a wavefront
     __shared__ float s_scale[E4M3 ? BT : 1];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = all_waves & 3, grp = KG > 1 ? all_waves >> 2 : 0;
     const int g = lane / MT, r = lane % MT;
 
     // blocks are dealt to the 8 XCDs in turn: give each a contiguous run of
@@ -334,8 +339,11 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     if constexpr (E4M3) {
         if ((int)threadIdx.x < BT) s_scale[threadIdx.x] = a.x_scale[min(t0 + (int)threadIdx.x, a.T - 1)];
     }
-    const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + n0 * a.ldw, a.ldw, min(BN, a.N - n0), a.chunks);
-    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + t0 * a.ldx, a.ldx, min(BT, a.T - t0), a.chunks);
+    // this split's steps of k (all of them unless k is divided)
+    const int step0 = blockIdx.y * a.split_steps;
+    const int chunks = min(a.chunks - 8 * step0, 8 * a.split_steps), steps = (chunks + 8 * KG - 1) / (8 * KG);
+    const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + n0 * a.ldw + 128 * step0, a.ldw, min(BN, a.N - n0), chunks);
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + t0 * a.ldx + 128 * step0, a.ldx, min(BT, a.T - t0), chunks);
     const int lr = lane >> 3, lc = (lane & 7) ^ ((lr >> 1) + 4 * (wave & 1));   // row within a load, chunk of it
     uint32_t off_x[LX], off_a[LW], off_b[LW];
 #pragma unroll
@@ -351,20 +359,22 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     }
     // load i of a part of step `step` (zeros past the last chunk)
     auto fetch = [&](uint32_t off, const __amdgpu_buffer_rsrc_t &rsrc, i32x4 *s, int i, int step) {
+        // uniform, but not always seen to be: a divergent scalar offset would become a loop over lanes
+        const int at = __builtin_amdgcn_readfirstlane(step * KG + grp);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(s + (i * 4 + wave) * 64), 16,
-                                                 8 * step + lc < a.chunks ? off : kOutside, 128 * step, 0, 0);
+                                                 8 * at + lc < chunks ? off : kOutside, 128 * at, 0, 0);
     };
     // loads [i0, i1) of X, then WA; of WB
     auto fetch_xa = [&](auto st, int i0, int i1, int step) {
 #pragma unroll
         for (int i = i0; i < i1; ++i) {
-            if (i < LX) fetch(off_x[i], rx, part<E4M3, BN, BT, MT, decltype(st)::value, 0>(), i, step);
-            else fetch(off_a[i - LX], rw, part<E4M3, BN, BT, MT, decltype(st)::value, 1>(), i - LX, step);
+            if (i < LX) fetch(off_x[i], rx, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 0>() + grp * (BT * 8)), i, step);
+            else fetch(off_a[i - LX], rw, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 1>() + grp * (BN * 4)), i - LX, step);
         }
     };
     auto fetch_b = [&](auto st, int i0, int i1, int step) {
 #pragma unroll
-        for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, part<E4M3, BN, BT, MT, decltype(st)::value, 2>(), i, step);
+        for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 2>() + grp * (BN * 4)), i, step);
     };
     const int swz = (r >> 1) & 7;
     const int at_x = ((wave & 1) * (BT / 2) + r) * 8, at_w = ((wave >> 1) * (BN / 4) + r) * 8;
@@ -377,7 +387,6 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[h][j][i] = (typename S::Acc)(0.0f);
 
-    const int steps = (a.chunks + 7) / 8;
     typename S::Operand x[P][FT], wa[P][HN], wb[P][HN];
     constexpr int XA = LX + LW;
     fetch_xa(Const<0>{}, 0, XA, 0);
@@ -395,9 +404,9 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
     for (int h = 0; h < P; ++h) {
 #pragma unroll
-        for (int j = 0; j < FT; ++j) x[h][j] = read(part<E4M3, BN, BT, MT, 0, 0>(), at_x + j * (MT * 8), h);
+        for (int j = 0; j < FT; ++j) x[h][j] = read((part<E4M3, BN, BT, MT, KG, 0, 0>() + grp * (BT * 8)), at_x + j * (MT * 8), h);
 #pragma unroll
-        for (int i = 0; i < HN; ++i) wa[h][i] = read(part<E4M3, BN, BT, MT, 0, 1>(), at_w + i * (MT * 8), h);
+        for (int i = 0; i < HN; ++i) wa[h][i] = read((part<E4M3, BN, BT, MT, KG, 0, 1>() + grp * (BN * 4)), at_w + i * (MT * 8), h);
     }
     // Step k, its parts in stage st.  The scheduling barriers keep each token
     // tile's few loads and reads among its matrix instructions.
@@ -408,7 +417,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
-            if (q < P * HN) wb[q / HN][q % HN] = read(part<E4M3, BN, BT, MT, ST, 2>(), at_w + q % HN * (MT * 8), q / HN);
+            if (q < P * HN) wb[q / HN][q % HN] = read((part<E4M3, BN, BT, MT, KG, ST, 2>() + grp * (BN * 4)), at_w + q % HN * (MT * 8), q / HN);
             fetch_b(Const<LAST>{}, q * LW / (P * FT), (q + 1) * LW / (P * FT), k + B - 1);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[0][j][i] = S::mma(wa[h][i], x[h][j], acc[0][j][i]);
@@ -419,11 +428,11 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
-            if (q < P * HN) wa[q / HN][q % HN] = read(part<E4M3, BN, BT, MT, NEXT, 1>(), at_w + q % HN * (MT * 8), q / HN);
+            if (q < P * HN) wa[q / HN][q % HN] = read((part<E4M3, BN, BT, MT, KG, NEXT, 1>() + grp * (BN * 4)), at_w + q % HN * (MT * 8), q / HN);
             fetch_xa(st, q * XA / (P * FT), (q + 1) * XA / (P * FT), k + B);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[1][j][i] = S::mma(wb[h][i], x[h][j], acc[1][j][i]);
-            x[h][j] = read(part<E4M3, BN, BT, MT, NEXT, 0>(), at_x + j * (MT * 8), h);
+            x[h][j] = read((part<E4M3, BN, BT, MT, KG, NEXT, 0>() + grp * (BT * 8)), at_x + j * (MT * 8), h);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -448,12 +457,44 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     }
     arrive<0>();                                                 // no load is on its way to LDS any more
 
+    if constexpr (KG > 1) {
+        // the groups' sums meet in LDS, [group][token][output], two groups a
+        // stage of X; then a lane finishes 8 outputs of a token
+        constexpr int ROW = BN / 4, ITEMS = BT * BN / 8;         // 4-output chunks of a token; lanes of work
+        static_assert(KG == 4 && MT == 16 && 2 * BT * ROW <= KG * BT * 8, "two groups' sums fit a stage");
+        i32x4 *const x0 = part<E4M3, BN, BT, MT, KG, 0, 0>(), *const x1 = part<E4M3, BN, BT, MT, KG, 1, 0>();
+        i32x4 *mine = (grp & 2 ? x1 : x0) + (grp & 1) * (BT * ROW);
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+#pragma unroll
+            for (int i = 0; i < 2 * HN; ++i) {
+                const int t = (wave & 1) * (BT / 2) + 16 * j + r, c = (wave >> 1) * (ROW / 2) + 4 * i + g;
+                mine[t * ROW + (c ^ (t & 7))] = __builtin_bit_cast(i32x4, acc[i / HN][j][i % HN]);
+            }
+        __syncthreads();
+        for (int o = threadIdx.x; o < ITEMS; o += 256 * KG) {
+            const int t = o / (BN / 8), c = o % (BN / 8) * 2;
+            Columns<E4M3> cols;
+            cols.load(a, n0 + 4 * c);
+            const half8 res = a.planes ? half8{} : cols.residual(a, t0 + t);
+            f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+#pragma unroll
+            for (int q = 0; q < KG; ++q) {
+                const i32x4 *p = (q & 2 ? x1 : x0) + (q & 1) * (BT * ROW) + t * ROW;
+                lo += __builtin_bit_cast(f32x4, p[c ^ (t & 7)]);
+                hi += __builtin_bit_cast(f32x4, p[(c + 1) ^ (t & 7)]);
+            }
+            if (a.planes) cols.store_plane(a, blockIdx.y, t0 + t, lo, hi);
+            else cols.finish(a, t0 + t, lo, hi, E4M3 ? s_scale[t] : 1.0f, res);
+        }
+        return;
+    } else {
     // Epilogue: the sums pass through LDS, 2 x 16 tokens of a wavefront at a
     // time, so that a lane finishes 8 neighbouring outputs of a token.
     constexpr int CW = BN / 8;                                   // 4-output chunks of a wavefront's row
     constexpr int PT = 32 / MT;                                  // token tiles at a time
     static_assert(32 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
-    i32x4 *mine = ((wave & 2) ? part<E4M3, BN, BT, MT, 1, 0>() : part<E4M3, BN, BT, MT, 0, 0>()) + (wave & 1) * (32 * CW);
+    i32x4 *mine = ((wave & 2) ? (part<E4M3, BN, BT, MT, KG, 1, 0>() + grp * (BT * 8)) : (part<E4M3, BN, BT, MT, KG, 0, 0>() + grp * (BT * 8))) + (wave & 1) * (32 * CW);
     constexpr int LPT = CW / 2, TPI = 64 / LPT;                  // lanes a token, tokens at once
     Columns<E4M3> cols;
     const int lane_n = lane % LPT;
@@ -479,56 +520,114 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
         // the next token's sums and residuals are asked for before this one's are finished
         int t = lane / LPT;
         const int t_first = t_wave + p * 32;
-        half8 res = cols.residual(a, t0 + t_first + t);
+        half8 res = a.planes ? half8{} : cols.residual(a, t0 + t_first + t);
         i32x4 lo = mine[t * CW + ((2 * lane_n) ^ (t & 7))], hi = mine[t * CW + ((2 * lane_n + 1) ^ (t & 7))];
 #pragma unroll 1
         for (; t < 32; t += TPI) {
             const int tn = min(t + TPI, 31);
-            const half8 res_next = cols.residual(a, t0 + t_first + tn);
+            const half8 res_next = a.planes ? half8{} : cols.residual(a, t0 + t_first + tn);
             const i32x4 lo_next = mine[tn * CW + ((2 * lane_n) ^ (tn & 7))];
             const i32x4 hi_next = mine[tn * CW + ((2 * lane_n + 1) ^ (tn & 7))];
-            cols.finish(a, t0 + t_first + t, __builtin_bit_cast(f32x4, lo), __builtin_bit_cast(f32x4, hi),
-                        E4M3 ? s_scale[t_first + t] : 1.0f, res);
+            const f32x4 lo_f = __builtin_bit_cast(f32x4, lo), hi_f = __builtin_bit_cast(f32x4, hi);
+            if (a.planes) cols.store_plane(a, blockIdx.y, t0 + t_first + t, lo_f, hi_f);
+            else cols.finish(a, t0 + t_first + t, lo_f, hi_f, E4M3 ? s_scale[t_first + t] : 1.0f, res);
             res = res_next;
             lo = lo_next;
             hi = hi_next;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
+    }
 }
 
-template <bool E4M3, int BN, int BT, int MT, int B>
-__global__ __launch_bounds__(256, BN + BT > 256 ? 1 : 2) void linear_tile_kernel(LinearArgs a, int tiles_n, int tiles_t)
+template <bool E4M3, int BN, int BT, int MT, int B, int KG>
+__global__ __launch_bounds__(256 * KG, BN + BT > 256 ? 1 : 2) void linear_tile_kernel(LinearArgs a, int tiles_n, int tiles_t)
 {
-    linear_tile<E4M3, BN, BT, MT, B>(a, tiles_n, tiles_t);
+    linear_tile<E4M3, BN, BT, MT, B, KG>(a, tiles_n, tiles_t);
 }
 
-template <bool E4M3, int FT>
-void launch_stream(const LinearArgs &a, hipStream_t s)
-{
-    const dim3 grid((unsigned int)((a.N + 15) / 16), (unsigned int)((a.T + 16 * FT - 1) / (16 * FT)));
-    hipLaunchKernelGGL((linear_stream_kernel<E4M3, FT, 8>), grid, dim3(512), 0, s, a);
-}
-
-template <bool E4M3, int BN, int BT, int MT, int B>
-void launch_tile(const LinearArgs &a, hipStream_t s)
-{
-    const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT;
-    hipLaunchKernelGGL((linear_tile_kernel<E4M3, BN, BT, MT, B>), dim3((unsigned int)(tn * tt)), dim3(256), 0, s, a, tn, tt);
-}
-
+// ------------------------------------------------------------ k divided
+// Sums the splits' planes in their order and finishes: one lane 8 outputs of a
+// token.
 template <bool E4M3>
-void launch(const LinearArgs &a, hipStream_t s)
+__global__ __launch_bounds__(256) void linear_join_kernel(LinearArgs a, int splits)
 {
-    if (a.T <= 16) return launch_stream<E4M3, 1>(a, s);
-    if (a.T <= 32) return launch_stream<E4M3, 2>(a, s);
-    if (a.T <= 64) return launch_stream<E4M3, 4>(a, s);
-    const long long big = (long long)((a.N + 255) / 256) * ((a.T + 255) / 256);
-    const long long mid = (long long)((a.N + 127) / 128) * ((a.T + 127) / 128);
-    if (big >= 200) return launch_tile<E4M3, 256, 256, E4M3 ? 16 : 32, 2>(a, s);
-    if (mid > 256) return launch_tile<E4M3, 128, 128, E4M3 ? 16 : 32, 2>(a, s);
-    if (mid >= 128) return launch_tile<E4M3, 128, 128, E4M3 ? 16 : 32, 4>(a, s);
-    launch_tile<E4M3, 64, 64, 16, 4>(a, s);
+    const int per_token = a.plane_ld / 8;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int t = (int)(i / per_token), c = (int)(i % per_token);
+    if (t >= a.T) return;
+    const f32x4 *p = reinterpret_cast<const f32x4 *>(a.planes + (long long)t * a.plane_ld + 8 * c);
+    const long long stride = (long long)a.T * a.plane_ld / 4;
+    Columns<E4M3> cols;
+    cols.load(a, 8 * c);
+    const half8 res = cols.residual(a, t);
+    const float sx = E4M3 ? a.x_scale[t] : 1.0f;
+    f32x4 lo = p[0], hi = p[1];
+#pragma unroll 4
+    for (int s = 1; s < splits; ++s) {
+        lo += p[s * stride];
+        hi += p[s * stride + 1];
+    }
+    cols.finish(a, t, lo, hi, sx, res);
+}
+
+// Splits of k: only for long sums (kSplitFrom 128-byte steps or more: 8192 FP16 or
+// 16384 e4m3 values), into parts of kSplitSteps steps or more, until the blocks
+// fill the 256 CUs, with planes of at most kPlaneBytes in all.  The second launch
+// costs what about 100 steps of one block take: 64 x 512 x 8192 FP16 15.2 us in
+// one part, 9.9 in 4; 64 x 512 x 8192 e4m3 (64 steps) 9.7 in one, 10.1 in 2.
+constexpr int kSplitFrom = 128, kSplitSteps = 32, kMaxSplits = 16;
+constexpr long long kPlaneBytes = 32 << 20;
+
+int plane_ld(int N) { return (N + 7) / 8 * 8; }
+
+int splits_of(const LinearArgs &a, long long tiles)
+{
+    const int steps = (a.chunks + 7) / 8;
+    if (steps < kSplitFrom) return 1;
+    const long long plane = (long long)a.T * plane_ld(a.N) * 4;
+    const long long want = min(min(256 / tiles, kPlaneBytes / plane), (long long)min(kMaxSplits, steps / kSplitSteps));
+    if (want <= 1) return 1;
+    const int per = (int)((steps + want - 1) / want);
+    return (steps + per - 1) / per;              // no split is empty
+}
+
+template <bool E4M3, int BN, int BT, int MT, int B, int KG = 1>
+void launch_tile(LinearArgs a, int splits, void *ws, hipStream_t s)
+{
+    const int tn = (a.N + BN - 1) / BN, tt = (a.T + BT - 1) / BT, steps = (a.chunks + 7) / 8;
+    a.split_steps = (steps + splits - 1) / splits;
+    a.planes = splits > 1 ? (float *)ws : nullptr;
+    a.plane_ld = plane_ld(a.N);
+    hipLaunchKernelGGL((linear_tile_kernel<E4M3, BN, BT, MT, B, KG>), dim3((unsigned int)(tn * tt), (unsigned int)splits),
+                       dim3(256 * KG), 0, s, a, tn, tt);
+    if (splits > 1) {
+        const long long lanes = (long long)a.T * (a.plane_ld / 8);
+        hipLaunchKernelGGL(linear_join_kernel<E4M3>, dim3((unsigned int)((lanes + 255) / 256)), dim3(256), 0, s, a, splits);
+    }
+}
+
+// Which kernel: by the number of tiles, the smallest tile that keeps the 256 CUs
+// in one round (or two blocks a CU), as a larger one leaves CUs idle and a
+// smaller one reads its operands more often.  Measured (us, FP16 / e4m3):
+//   16 x 2048 x 2048: stream 6.1 / 4.6, 64 x 32 tiles 8.1 / 5.7
+//   32 x 5632 x 2048: stream 13.2 / 9.3, 64 x 32 tiles 8.8 / 6.6
+//   256 x 2048 x 2048: 64 x 32 tiles 7.4 / 5.9, 64 x 64 9.1 / 6.5, 128 x 128 16.4 / 12.3
+//   256 x 5632 x 2048: 64 x 32 tiles 21.4 / 15.1, 64 x 64 13.5 / 9.0, 128 x 128 17.4 / 12.7
+template <bool E4M3>
+void launch(const LinearArgs &a, void *ws, hipStream_t s)
+{
+    auto tiles = [&](int bn, int bt) { return (long long)((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt); };
+    constexpr int LARGE = E4M3 ? 16 : 32;        // FP16 accumulators of 16 x 16 tiles do not stay in place
+    if (a.T <= kStreamT) {
+        hipLaunchKernelGGL((linear_stream_kernel<E4M3, 8>), dim3((unsigned int)((a.N + 15) / 16)), dim3(512), 0, s, a);
+        return;
+    }
+    if (tiles(64, 32) <= 256) return launch_tile<E4M3, 64, 32, 16, 2, 4>(a, splits_of(a, tiles(64, 32)), ws, s);
+    if (tiles(64, 64) <= 512) return launch_tile<E4M3, 64, 64, 16, 4>(a, 1, ws, s);
+    if (tiles(256, 256) >= 200) return launch_tile<E4M3, 256, 256, LARGE, 2>(a, 1, ws, s);
+    if (tiles(128, 128) > 256) return launch_tile<E4M3, 128, 128, LARGE, 2>(a, 1, ws, s);
+    launch_tile<E4M3, 128, 128, LARGE, 4>(a, 1, ws, s);
 }
 
 constexpr int kMaxLd = 1 << 22;                  // elements: 256 rows stay within 32-bit offsets
@@ -542,7 +641,9 @@ size_t moe_linear_workspace_size(int T, int N, int K, int type)
 {
     if (T < 0 || T > 65536 || N < 1 || N > kMaxN || K < 16 || K > kMaxK || K % 16) return 0;
     if (type != MOE_LINEAR_FP16 && type != MOE_LINEAR_E4M3) return 0;
-    return 256;
+    // the planes of every T' <= T
+    const long long most = (long long)kMaxSplits * T * plane_ld(N) * 4;
+    return 256 + (size_t)(most < kPlaneBytes ? most : kPlaneBytes);
 }
 
 int moe_linear(const void *x_dev, long long ldx, const float *x_scale_dev, const void *w_dev, long long ldw,
@@ -593,8 +694,10 @@ int moe_linear(const void *x_dev, long long ldx, const float *x_scale_dev, const
     a.N = N;
     a.chunks = K * size / 16;
     a.act = act;
-    if (e4m3) launch<true>(a, (hipStream_t)stream);
-    else launch<false>(a, (hipStream_t)stream);
+    a.planes = nullptr;
+    a.plane_ld = a.split_steps = 0;
+    if (e4m3) launch<true>(a, ws_dev, (hipStream_t)stream);
+    else launch<false>(a, ws_dev, (hipStream_t)stream);
     return moe::check_launch(who);
 }
 
