@@ -118,3 +118,17 @@ def test_linear_refusals():
     for args in ((-1, 8, 16, 0), (4, 0, 16, 0), (4, 8, 8, 0), (4, 8, 24, 1), (4, 8, 16, 2)):
         assert B.moe_linear_workspace_size(*args) == 0
     linear(T=0, x=None, w=None, y=None, ws=None, ws_bytes=0)    # nothing to do
+
+
+def test_host_tensors_are_refused():
+    # a host address would fault the GPU: refused before anything is enqueued
+    import torch
+    h = torch.zeros(4, 256, dtype=torch.float16)
+    with pytest.raises(ValueError, match="GPU memory"):
+        B.moe_residual_rmsnorm(h, None, F, 1e-5, 4, 256, norm=F, stream=0)
+    with pytest.raises(ValueError, match="one GPU"):
+        B.moe_residual_rmsnorm(F, None, h, 1e-5, 4, 256, norm=F, stream=0)
+    with pytest.raises(ValueError, match="GPU memory"):
+        B.moe_linear(h, F, 4, 64, 256, B.MOE_LINEAR_FP16, F, ws=F, ws_bytes=1 << 30, stream=0)
+    with pytest.raises(ValueError, match="one GPU"):
+        B.moe_route_scored(F, h, None, 4, 256, 8, 2, B.route_rule(), None, F, F, F, F, F, F, F, F, 1 << 20, stream=0)

@@ -10,7 +10,6 @@ raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -257,22 +256,22 @@ def _g(t, dev: int):
     if t is None or isinstance(t, int):
         return t
     d = t.get_device()
-    if d != dev and (d < 0 or dev >= 0):
+    if d < 0 or (d != dev and dev >= 0):
         raise ValueError("the tensors of a call must be on one GPU")
     return t.data_ptr()
 
 
-def _on_its_device(call):
-    """Runs `call` with its first argument's device current, so that its stream and launches are that device's."""
-    @functools.wraps(call)
-    def run(x, *args, **kw):
-        d = _device(x)
-        if d >= 0 and d != _c()._cuda_getDevice():
-            import torch
-            with torch.cuda.device(d):
-                return call(x, *args, **kw)
-        return call(x, *args, **kw)
-    return run
+def _elsewhere(d: int) -> bool:
+    """Whether tensors of device d (_device) are on another device than the current one."""
+    return d >= 0 and d != _c()._cuda_getDevice()
+
+
+def _there(d: int, call, args: dict):
+    """`call` with device d current, so that its stream and launches are that device's."""
+    import torch
+    del args["d"]
+    with torch.cuda.device(d):
+        return call(**args)
 
 
 def _check(rc: int):
@@ -336,10 +335,11 @@ def route_rule(score=MOE_SCORE_SOFTMAX, n_group=1, topk_group=1, group_score=MOE
     return RouteRule(score, n_group, topk_group, group_score, 1 if renormalize else 0, scale)
 
 
-@_on_its_device
 def moe_route_scored(x, w_router, select_bias, T, H, E, k, rule: RouteRule, logits, topk_ids, topk_w, expert_offsets,
                      sorted_pairs, pair_pos, active_list, n_active, ws, ws_bytes, stream=None):
     d = _device(x)
+    if _elsewhere(d):
+        return _there(d, moe_route_scored, locals())
     _check(load().moe_route_scored(_g(x, d), _g(w_router, d), _g(select_bias, d), T, H, E, k,
                                    None if rule is None else ctypes.byref(rule), _g(logits, d), _g(topk_ids, d),
                                    _g(topk_w, d), _g(expert_offsets, d), _g(sorted_pairs, d), _g(pair_pos, d),
@@ -457,11 +457,12 @@ def _ld(t, ld, width):
     return width if st[0] < width and t.shape[0] == 1 else st[0]
 
 
-@_on_its_device
 def moe_residual_rmsnorm(x, y, w, eps, T, H, sum_out=None, norm=None, q=None, q_scale=None, ldx=None, ldy=None,
                          ld_sum=None, ld_norm=None, ldq=None, stream=None):
     """Row strides (elements) are those of 2-D tensors unless given."""
     d = _device(x)
+    if _elsewhere(d):
+        return _there(d, moe_residual_rmsnorm, locals())
     _check(load().moe_residual_rmsnorm(_g(x, d), _ld(x, ldx, H), _g(y, d), _ld(y, ldy, H), _g(w, d), eps, T, H,
                                        _g(sum_out, d), _ld(sum_out, ld_sum, H), _g(norm, d), _ld(norm, ld_norm, H),
                                        _g(q, d), _ld(q, ldq, H), _g(q_scale, d), _s(stream)))
@@ -471,11 +472,12 @@ def moe_linear_workspace_size(T: int, N: int, K: int, type: int) -> int:
     return int(load().moe_linear_workspace_size(T, N, K, type))
 
 
-@_on_its_device
 def moe_linear(x, w, T, N, K, type, y, x_scale=None, w_scale=None, bias=None, act=MOE_ACT_NONE, residual=None,
                ws=None, ws_bytes=0, ldx=None, ldw=None, ldr=None, ldy=None, stream=None):
     """Row strides (elements) are those of 2-D tensors unless given."""
     d = _device(x)
+    if _elsewhere(d):
+        return _there(d, moe_linear, locals())
     _check(load().moe_linear(_g(x, d), _ld(x, ldx, K), _g(x_scale, d), _g(w, d), _ld(w, ldw, K), _g(w_scale, d),
                              _g(bias, d), _g(residual, d), _ld(residual, ldr, N), T, N, K, type, act, _g(y, d),
                              _ld(y, ldy, N), _g(ws, d), ws_bytes, _s(stream)))
