@@ -19,12 +19,21 @@ class RoutedExpertLayer:
     router: float16 CUDA tensor [H, E].  bias: float32 CUDA tensor [E] or None.
     slot_map: int32 CUDA tensor [E] (slot of each expert, -1 = absent) or None
     (expert e in slot e).
+    rule: None (moe_route: softmax over the k chosen logits) or a routing rule
+    (binding.route_rule): the layer then routes by scores (moe_route_scored) with
+    select_bias, float32 CUDA tensor [E] or None, and takes no logit bias.
     """
 
     def __init__(self, H: int, I: int, E: int, k: int, rows: torch.Tensor, router: torch.Tensor,
                  bias: torch.Tensor | None = None, slot_map: torch.Tensor | None = None, max_T: int = 64,
-                 device: str | torch.device = "cuda:0"):
+                 device: str | torch.device = "cuda:0", rule: "B.RouteRule | None" = None,
+                 select_bias: torch.Tensor | None = None):
+        if rule is not None and bias is not None:
+            raise ValueError("routing by scores takes no logit bias (select_bias biases the choice)")
+        if rule is None and select_bias is not None:
+            raise ValueError("select_bias goes with a routing rule")
         self.H, self.I, self.E, self.k = H, I, E, k
+        self.rule, self.select_bias = rule, select_bias
         self.row_bytes, self.offsets6 = B.moe_expert_row_bytes(H, I)
         if rows.dtype != torch.uint8 or rows.dim() != 2 or rows.shape[1] < self.row_bytes:
             raise ValueError("rows must be uint8 [n_slots, >= row_bytes]")
@@ -48,6 +57,9 @@ class RoutedExpertLayer:
         self.n_active = torch.empty(1, dtype=torch.int32, device=d)
         self.ws_bytes = B.moe_route_workspace_size(T, H, E)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=d)
+        # workspace of the routing by scores: zero-filled once, its counters left zero by every call
+        self.scored_ws = None if self.rule is None else torch.zeros(B.moe_route_scored_workspace_size(T, H, E),
+                                                                    dtype=torch.uint8, device=d)
         self.h = torch.empty((n, I), dtype=torch.float16, device=d)
         self.pair_out = torch.empty((n, H), dtype=torch.float32, device=d)
         self.status = torch.zeros(1, dtype=torch.int32, device=d)
@@ -71,7 +83,13 @@ class RoutedExpertLayer:
         T = x.shape[0]
         if T > self.max_T:
             self._alloc(T)
-        if exact:
+        if self.rule is not None:
+            if exact:
+                raise ValueError("the integer routing path has no scores")
+            B.moe_route_scored(x, self.router, self.select_bias, T, self.H, self.E, self.k, self.rule, self.logits,
+                               self.topk_ids, self.topk_w, self.expert_offsets, self.sorted_pairs, self.pair_pos,
+                               self.active_list, self.n_active, self.scored_ws, self.scored_ws.numel(), stream)
+        elif exact:
             B.moe_route_exact(x, self.router, self.bias, T, self.H, self.E, self.k, self.logits, self.topk_ids,
                               self.topk_w, self.expert_offsets, self.sorted_pairs, self.pair_pos, self.active_list,
                               self.n_active, self.ws, self.ws_bytes, stream)
@@ -134,6 +152,25 @@ class RoutedExpertLayer:
         self.combine(T, y, shared_out, shared_gate, main)
         return y
 
+    def _separate(self, x, y, stream, rows, lease, shared, mode):
+        """Route, expert FFN (beside the shared expert on its side stream) and combine as calls of
+        their own."""
+        T = x.shape[0]
+        if y is None:
+            y = torch.empty((T, self.H), dtype=torch.float16, device=self.device)
+        main = _torch_stream(stream)
+        if shared is not None:
+            shared.side_stream().wait_stream(main)
+            shared.run(x, shared.side_stream())
+        self.route(x, main)
+        self.ffn(x, main, rows, lease, mode)
+        if shared is not None:
+            main.wait_stream(shared.side_stream())
+            self.combine(T, y, shared.out, shared.gate, main)
+        else:
+            self.combine(T, y, stream=main)
+        return y
+
     def forward_fused(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None, rows=None, lease=None,
                       shared: "SharedExpert | None" = None, mode: int = B.MOE_FFN_PATH_AUTO) -> torch.Tensor:
         """y = layer(x) through the one-call layer (moe_layer_forward: three or four launches for
@@ -142,8 +179,11 @@ class RoutedExpertLayer:
         on a second stream beside the routed work and the combine waits for its event (for
         decode batches forward_shared, which runs both on one stream with the shared gate/up
         pass inside the routing launch, was measured faster: Qwen shape T = 1 40.6 against
-        48.9 us, T = 16 72.5 against 80.4)."""
+        48.9 us, T = 16 72.5 against 80.4).  A layer with a routing rule runs its separate
+        calls (the one-call layer routes by moe_route)."""
         T = x.shape[0]
+        if self.rule is not None:
+            return self._separate(x, y, stream, rows, lease, shared, mode)
         if T > self.max_T:
             self._alloc(T)
         if y is None:
@@ -171,8 +211,11 @@ class RoutedExpertLayer:
                        rows=None, lease=None, mode: int = B.MOE_FFN_PATH_AUTO) -> torch.Tensor:
         """y = layer(x) with the shared expert, all on one stream (moe_layer_forward_shared): for
         decode batches the routing launch also runs the shared expert's gate/up pass; the
-        result equals forward_fused's with the same shared expert."""
+        result equals forward_fused's with the same shared expert.  A layer with a routing rule
+        runs its separate calls."""
         T = x.shape[0]
+        if self.rule is not None:
+            return self._separate(x, y, stream, rows, lease, shared, mode)
         if T > self.max_T:
             self._alloc(T)
         if y is None:
@@ -361,6 +404,55 @@ class ResidentExpertTable:
             pass
 
 
+class DenseFFN:
+    """A dense layer of a stack (moe_linear twice): h = act(x W_up^T + b_up), out = h W_down^T +
+    b_down + residual.
+
+    w_up: CUDA tensor [I, H], float16, or float8_e4m3fn with up_scale (float32 [I]): the layer then
+    takes 8-bit activations with their scales (moe_residual_rmsnorm's q and q_scale).  w_down:
+    float16 [H, I].  up_bias, down_bias: float32 or None.  act: a binding MOE_ACT_* value.
+    """
+
+    def __init__(self, w_up: torch.Tensor, w_down: torch.Tensor, up_scale: torch.Tensor | None = None,
+                 up_bias: torch.Tensor | None = None, down_bias: torch.Tensor | None = None,
+                 act: int = B.MOE_ACT_SILU, device: str | torch.device = "cuda:0"):
+        self.I, self.H = w_up.shape
+        self.e4m3 = w_up.dtype == torch.float8_e4m3fn
+        if not self.e4m3 and w_up.dtype != torch.float16 or w_down.dtype != torch.float16:
+            raise ValueError("w_up must be float16 or float8_e4m3fn, w_down float16")
+        if tuple(w_down.shape) != (self.H, self.I) or self.e4m3 != (up_scale is not None):
+            raise ValueError("w_down must be [H, I], and up_scale goes with e4m3 weights")
+        self.w_up, self.w_down, self.up_scale = w_up, w_down, up_scale
+        self.up_bias, self.down_bias, self.act = up_bias, down_bias, act
+        self.device = torch.device(device)
+        self.max_T = -1
+
+    def _ensure(self, T: int):
+        if T <= self.max_T:
+            return
+        self.max_T = T
+        self.h = torch.empty((max(T, 1), self.I), dtype=torch.float16, device=self.device)
+        up = B.MOE_LINEAR_E4M3 if self.e4m3 else B.MOE_LINEAR_FP16
+        need = max(B.moe_linear_workspace_size(T, self.I, self.H, up),
+                   B.moe_linear_workspace_size(T, self.H, self.I, B.MOE_LINEAR_FP16))
+        self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def run(self, x: torch.Tensor, x_scale: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+            out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """x: float16 [T, H], or the 8-bit activations with x_scale (float32 [T])."""
+        T = x.shape[0]
+        self._ensure(T)
+        if out is None:
+            out = torch.empty((T, self.H), dtype=torch.float16, device=self.device)
+        n = self.ws.numel()
+        B.moe_linear(x, self.w_up, T, self.I, self.H, B.MOE_LINEAR_E4M3 if self.e4m3 else B.MOE_LINEAR_FP16, self.h,
+                     x_scale=x_scale, w_scale=self.up_scale, bias=self.up_bias, act=self.act, ws=self.ws, ws_bytes=n,
+                     stream=stream)
+        B.moe_linear(self.h, self.w_down, T, self.H, self.I, B.MOE_LINEAR_FP16, out, bias=self.down_bias,
+                     residual=residual, ws=self.ws, ws_bytes=n, stream=stream)
+        return out
+
+
 class DecodeStack:
     """Decode through a stack of routed-expert layers with partial residency, chained by the
     residual stream: x_{l+1} = RN16(x_l + y_l) (moe_residual_add).
@@ -376,27 +468,65 @@ class DecodeStack:
     Experimental Evidence and Scope", "Architecture comparison matrix", row "Publication/staging
     semantics"); predicting from the residual stream is this implementation's reading.
     Results do not depend on prefetching: the same kernels read the same bytes.
+
+    norms: None (a layer reads the residual stream itself), or one float16 weight [H] per layer:
+    layer l then reads the root-mean-square norm of x_l, and the residual addition and the next
+    layer's norm are one launch (moe_residual_rmsnorm).  A layer may be a DenseFFN (its table None):
+    its residual addition is in its second product, and the norm before one with e4m3 weights
+    writes 8-bit activations.
     """
 
-    def __init__(self, layers, tables, shared=None, prefetch: bool = False):
+    def __init__(self, layers, tables, shared=None, prefetch: bool = False, norms=None, eps: float = 1e-5):
         self.layers, self.tables = list(layers), list(tables)
         self.shared = shared
         self.prefetch = prefetch
         self.L = len(self.layers)
+        self.norms, self.eps = None if norms is None else list(norms), eps
+        if self.norms is not None and len(self.norms) != self.L:
+            raise ValueError("one norm weight per layer")
+        if self.norms is None and any(isinstance(l, DenseFFN) and l.e4m3 for l in self.layers):
+            raise ValueError("a dense layer with e4m3 weights needs norms (they make its 8-bit activations)")
         lay = self.layers[0]
         # predictors: the next layer's router (and bias) on buffers of their own
-        self.preds = [None] + [RoutedExpertLayer(l.H, l.I, l.E, l.k, l.rows, l.router, l.bias, max_T=l.max_T,
-                                                 device=l.device) for l in self.layers[1:]] if prefetch else None
+        self.preds = [None] + [None if isinstance(l, DenseFFN) else
+                               RoutedExpertLayer(l.H, l.I, l.E, l.k, l.rows, l.router, l.bias, max_T=l.max_T,
+                                                 device=l.device, rule=l.rule, select_bias=l.select_bias)
+                               for l in self.layers[1:]] if prefetch else None
         self.device = lay.device
+
+    def _advance(self, l: int, x, y, main):
+        """The residual stream x (+ y) and what layer l reads of it: (x_l, input, scales).  y None: x is
+        the stream already."""
+        T, H = x.shape
+        if self.norms is None or l == self.L:
+            if y is None:
+                return x, x, None
+            nxt = torch.empty_like(x)
+            B.moe_residual_add(x, y, nxt, T * H, main)
+            return nxt, nxt, None
+        e4m3 = isinstance(self.layers[l], DenseFFN) and self.layers[l].e4m3
+        total = x if y is None else torch.empty_like(x)
+        norm = torch.empty((T, H), dtype=torch.float8_e4m3fn if e4m3 else torch.float16, device=self.device)
+        scale = torch.empty(T, dtype=torch.float32, device=self.device) if e4m3 else None
+        B.moe_residual_rmsnorm(x, y, self.norms[l], self.eps, T, H, sum_out=None if y is None else total,
+                               norm=None if e4m3 else norm, q=norm if e4m3 else None, q_scale=scale, stream=main)
+        return total, norm, scale
 
     def step(self, x0: torch.Tensor, ys=None, timer=None) -> torch.Tensor:
         """Runs every layer on x0 (float16 [T, H]); returns x_L.  ys: optional list receiving each
-        layer's y (copies).  timer: optional callable(layer, phase) for event timing."""
+        layer's y (copies; a dense layer's x_{l+1}).  timer: optional callable(layer, phase) for event
+        timing."""
         T, H = x0.shape
-        x = x0
         main = torch.cuda.current_stream()
+        res, x, scale = self._advance(0, x0, None, main)
         for l in range(self.L):
             lay, tab = self.layers[l], self.tables[l]
+            if isinstance(lay, DenseFFN):
+                res = lay.run(x, scale, residual=res, stream=main)
+                if ys is not None:
+                    ys.append(res)
+                res, x, scale = self._advance(l + 1, res, None, main)
+                continue
             lay.route(x, main)
             nxt = self.preds[l + 1] if self.prefetch and l + 1 < self.L else None
             if nxt is not None:
@@ -428,7 +558,5 @@ class DecodeStack:
                 self.tables[l + 1].prefetch(predicted)
             if ys is not None:
                 ys.append(y)
-            x_next = torch.empty_like(x)
-            B.moe_residual_add(x, y, x_next, T * H, main)
-            x = x_next
-        return x
+            res, x, scale = self._advance(l + 1, res, y, main)
+        return res
