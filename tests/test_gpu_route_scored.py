@@ -270,3 +270,23 @@ def test_captured_replays(T):
         graph.replay()
         logits = oracle.router_logits(x2, wr)
         check(call.host(), expected(logits, k, bias, **rule), logits, f"replay {step}")
+
+
+@pytest.mark.parametrize("xs,ws", [(1.0, 1.0), (2.0 ** 6, 2.0 ** 4), (2.0 ** -15, 2.0 ** -12), (2.0 ** 13, 2.0 ** -18)],
+                         ids=["unit", "large", "subnormal", "mixed"])
+@pytest.mark.parametrize("T", [20, 130])
+def test_logits_are_correctly_rounded_at_every_magnitude(T, xs, ws):
+    """Sums that stay exact in fp64, sums that round, subnormal operands: the FP32 logits are those of
+    the exact sums."""
+    g = np.random.default_rng(31)
+    H, E = 2048, 64
+    x = (g.standard_normal((T, H)) * xs).astype(np.float16)
+    w = (g.standard_normal((H, E)) * ws).astype(np.float16)
+    w[:, 5] = -w[:, 4]                                 # cancelling halves: small logits of large terms
+    x[:, 1::2] = x[:, ::2]
+    w[1::2, 4] = -w[::2, 4]
+    w[1, 4] += np.float16(ws)
+    call = Call(T, H, E, 4)
+    call(*device(x, w), None, score=SIGMOID)
+    want = oracle.router_logits(x, w)
+    check(call.host(), expected(want, 4, None, score=SIGMOID), want, f"T={T}")
