@@ -14,6 +14,8 @@
 //   linear_join_kernel adds the splits in their order.
 #include "moe_internal.h"
 
+#include <algorithm>
+
 namespace {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
@@ -607,13 +609,28 @@ void launch_tile(LinearArgs a, int splits, void *ws, hipStream_t s)
     }
 }
 
-// Which kernel: by the number of tiles, the smallest tile that keeps the 256 CUs
-// in one round (or two blocks a CU), as a larger one leaves CUs idle and a
-// smaller one reads its operands more often.  Measured (us, FP16 / e4m3):
+// Time of `tiles` blocks where `slots` run at once and a full round takes `cost`: whole rounds, and
+// a last one that takes at least `least` of a full round, as a block alone is not that much faster.
+double rounds(long long tiles, int slots, double cost, double least)
+{
+    const double part = (double)(tiles % slots) / slots;
+    return cost * ((double)(tiles / slots) + (part > 0.0 ? least + (1.0 - least) * part : 0.0));
+}
+
+// Which kernel.  At most kStreamT tokens: the streaming kernel.  Then the 64 x 32 tiles (k in four
+// groups of wavefronts) while they fill no more than one round of the 256 CUs.  Then by the time of
+// the rounds, whose costs relative to 128 x 128 tiles with two blocks a CU are measured ones (FP16 72
+// us and e4m3 35 us a round at K 4096).  Measured (us, FP16 / e4m3; 128 x 128 with four stages (4)
+// and two (2)):
 //   16 x 2048 x 2048: stream 6.1 / 4.6, 64 x 32 tiles 8.1 / 5.7
 //   32 x 5632 x 2048: stream 13.2 / 9.3, 64 x 32 tiles 8.8 / 6.6
-//   256 x 2048 x 2048: 64 x 32 tiles 7.4 / 5.9, 64 x 64 9.1 / 6.5, 128 x 128 16.4 / 12.3
-//   256 x 5632 x 2048: 64 x 32 tiles 21.4 / 15.1, 64 x 64 13.5 / 9.0, 128 x 128 17.4 / 12.7
+//   256 x 2048 x 2048: 64 x 32 tiles 7.4 / 5.9, 64 x 64 9.1 / 6.5, 128 x 128 (4) 16.4 / 12.3
+//   256 x 5632 x 2048: 64 x 32 tiles 21.4 / 15.1, 64 x 64 13.5 / 9.0, 128 x 128 (4) 17.4 / 12.7
+//   512 x 5632 x 4096: 64 x 64 45 / 25, 128 x 128 (4) 35 / 22, (2) 41 / 25, 256 x 256 79 / 55
+//   2048 x 4096 x 4096: 128 x 128 (4) 81 / 45, (2) 72 / 36, 256 x 256 89 / 57
+//   2048 x 5632 x 4096: 128 x 128 (4) 125 / 65, (2) 127 / 58, 256 x 256 101 / 60
+//   4096 x 4096 x 4096: 128 x 128 (2) 145 / 70, 256 x 256 127 / 67
+//   70 x 65536 x 2048: 64 x 64 82 / 47, 128 x 128 (2) 74 / 34, 256 x 256 84 / 46
 template <bool E4M3>
 void launch(const LinearArgs &a, void *ws, hipStream_t s)
 {
@@ -624,10 +641,13 @@ void launch(const LinearArgs &a, void *ws, hipStream_t s)
         return;
     }
     if (tiles(64, 32) <= 256) return launch_tile<E4M3, 64, 32, 16, 2, 4>(a, splits_of(a, tiles(64, 32)), ws, s);
-    if (tiles(64, 64) <= 512) return launch_tile<E4M3, 64, 64, 16, 4>(a, 1, ws, s);
-    if (tiles(256, 256) >= 200) return launch_tile<E4M3, 256, 256, LARGE, 2>(a, 1, ws, s);
-    if (tiles(128, 128) > 256) return launch_tile<E4M3, 128, 128, LARGE, 2>(a, 1, ws, s);
-    launch_tile<E4M3, 128, 128, LARGE, 4>(a, 1, ws, s);
+    const double small = rounds(tiles(64, 64), 512, 0.45, 0.5), deep = rounds(tiles(128, 128), 256, 0.6, 0.5);
+    const double two = rounds(tiles(128, 128), 512, 1.0, 0.5), large = rounds(tiles(256, 256), 256, E4M3 ? 1.87 : 1.75, 0.65);
+    const double best = std::min(std::min(small, deep), std::min(two, large));
+    if (small == best) return launch_tile<E4M3, 64, 64, 16, 4>(a, 1, ws, s);
+    if (deep == best) return launch_tile<E4M3, 128, 128, LARGE, 4>(a, 1, ws, s);
+    if (two == best) return launch_tile<E4M3, 128, 128, LARGE, 2>(a, 1, ws, s);
+    launch_tile<E4M3, 256, 256, LARGE, 2>(a, 1, ws, s);
 }
 
 constexpr int kMaxLd = 1 << 22;                  // elements: 256 rows stay within 32-bit offsets

@@ -248,8 +248,16 @@ extern "C" int moe_residual_rmsnorm(const void *x_dev, long long ldx, const void
     a.eps = (double)eps;
     a.T = T; a.H = H;
     hipStream_t s = (hipStream_t)stream;
+    // Threads a row.  Few rows want more of them, for shorter chains of loads and sums; many want fewer
+    // reductions.  Measured (us, T = 1 / 64 / 1024 / 8192, FP16 outputs):
+    //   H 512: a wavefront 2.1 / 2.4 / 2.7 / 9.0, 256 threads 2.2 / 2.5 / 3.3 / 13.6
+    //   H 1024: a wavefront 2.5 / 2.9 / 4.4 / 13.8, 256 threads 2.3 / 2.5 / 4.6 / 18.1
+    //   H 2048: a wavefront 3.0 / 3.5 / 5.7 / 26.6, 256 threads 2.3 / 2.6 / 5.7 / 27.6
+    //   H 4096: 256 threads 2.8 / 3.1 / 8.8 / 52.3, 512 threads 2.6 / 2.8 / 9.3 / 49.6
+    //   H 8192: 256 threads 3.4 / 3.8 / 13.8 / 97.1, 1024 threads 3.2 / 3.7 / 17.5 / 94.2
+    //   H 16384: 256 threads 4.7 / 6.0 / 27.0 / 198, 1024 threads 3.9 / 5.5 / 28.2 / 196
     if (H <= 512) launch<64, 1>(a, s);
-    else if (H <= 1024) launch<64, 2>(a, s);
+    else if (H <= 1024 && T > 256) launch<64, 2>(a, s);
     else if (H <= 2048) launch<256, 1>(a, s);
     else if (H <= 4096) launch<256, 2>(a, s);
     else if (H <= 8192) launch<256, 4>(a, s);
