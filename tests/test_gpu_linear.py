@@ -233,3 +233,12 @@ def test_captured_replays_and_repeated_calls(T, N, K):
         assert torch.equal(y, eager), "a replay differs from the eager call"
         c.x = x.double().cpu().numpy()
         c.check(eager.cpu().numpy(), SILU, f"replay {step}")
+
+
+@pytest.mark.parametrize("type", [FP16, E4M3], ids=["fp16", "e4m3"])
+@pytest.mark.parametrize("T,N,K", [(1, 4111, 256), (5, 4100, 1040), (16, 5000, 2064), (9, 8193, 1040), (8, 8200, 1104),
+                                   (13, 9001, 2064), (16, 4097, 4112)])
+def test_few_tokens_and_many_outputs(T, N, K, type):
+    c = Case(T, N, K, type, whole=True)
+    c.check_whole(c.run(), f"{T}x{N}x{K}")
+    c.check_whole(c.run(ldx=K + 16, ldw=K + 48, ldy=N + 3, offset=1), f"{T}x{N}x{K} strided")

@@ -210,44 +210,53 @@ __device__ inline __amdgpu_buffer_rsrc_t rows_rsrc(const uint8_t *base, long lon
 constexpr uint32_t kOutside = 0xC0000000u;
 
 // ------------------------------------------------------------ at most 16 tokens
-// Block: 16 rows of W, all of k; wavefront w takes the 128-byte steps w, w + NW,
+// Block: 16 R rows of W, all of k; wavefront w takes the 128-byte steps w, w + NW,
 // ... and the NW partial sums meet in LDS.  Every lane asks for U steps of both
-// operands before it uses the first.
+// operands before it uses the first.  Bound by one round of loads for small W
+// (1 x 2048 x 2048 4.6 us FP16, 3.6 e4m3), by HBM for large ones (1 x 65536 x 2048
+// FP16 51 us, 5.2 TB/s; e4m3 26 us, 5.1 TB/s).
 constexpr int kStreamT = 16;
 
-template <bool E4M3, int NW>
+template <bool E4M3, int NW, int R>
 __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 {
     typedef Step<E4M3, 16> S;
     constexpr int U = 4;
+    static_assert(2 * kStreamT * R <= NW * 64, "two lanes a token and 16 rows");
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int g = lane >> 4, r = lane & 15;
-    const int n0 = blockIdx.x * 16;
-    __shared__ f32x4 s_acc[NW][64];
-    const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + n0 * a.ldw, a.ldw, min(16, a.N - n0), a.chunks);
+    const int n0 = blockIdx.x * (16 * R);
+    __shared__ f32x4 s_acc[NW][R][64];
+    const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + n0 * a.ldw, a.ldw, min(16 * R, a.N - n0), a.chunks);
     const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x, a.ldx, a.T, a.chunks);
-    const uint32_t row_w = n0 + r < a.N ? (uint32_t)(r * a.ldw) : kOutside;
+    uint32_t row_w[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) row_w[i] = n0 + 16 * i + r < a.N ? (uint32_t)((16 * i + r) * a.ldw) : kOutside;
     const uint32_t row_x = r < a.T ? (uint32_t)(r * a.ldx) : kOutside;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     // the epilogue's operands first: they arrive while the products are made.
-    // Two lanes a token: outputs 8h .. 8h + 7 are the results of lanes (2h, r) and (2h + 1, r)
-    const int et = tid >> 1, eh = tid & 1;
+    // Two lanes a token: outputs 8h .. 8h + 7 of 16 rows are the results of lanes (2h, r) and (2h + 1, r)
+    const int et = tid >> 1 & 15, eh = tid & 1, ei = tid >> 5;
     Columns<E4M3> cols;
     half8 res = {};
     float sx = 1.0f;
-    if (tid < 2 * kStreamT) {
-        cols.load(a, n0 + 8 * eh);
+    if (tid < 2 * kStreamT * R) {
+        cols.load(a, n0 + 16 * ei + 8 * eh);
         res = cols.residual(a, et);
         if constexpr (E4M3) sx = a.x_scale[min(et, a.T - 1)];
     }
     for (int s = wave; 8 * s < a.chunks; s += NW * U) {
-        i32x4 w[U][2], x[U][2];
+        i32x4 w[R][U][2], x[U][2];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int c = 8 * (s + u * NW) + 4 * h + g;
-                w[u][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, c < a.chunks ? row_w + 16u * c : kOutside, 0, 0);
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    w[i][u][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, c < a.chunks ? row_w[i] + 16u * c : kOutside, 0, 0);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -259,17 +268,20 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int h = 0; h < S::kParts; ++h) acc = S::mma(S::pick(w[u], h), S::pick(x[u], h), acc);
+            for (int h = 0; h < S::kParts; ++h)
+#pragma unroll
+                for (int i = 0; i < R; ++i) acc[i] = S::mma(S::pick(w[i][u], h), S::pick(x[u], h), acc[i]);
     }
-    s_acc[wave][lane] = acc;
+#pragma unroll
+    for (int i = 0; i < R; ++i) s_acc[wave][i][lane] = acc[i];
     __syncthreads();
-    if (tid < 2 * kStreamT) {
+    if (tid < 2 * kStreamT * R) {
         const int at = 32 * eh + et;
-        f32x4 lo = s_acc[0][at], hi = s_acc[0][at + 16];
+        f32x4 lo = s_acc[0][ei][at], hi = s_acc[0][ei][at + 16];
 #pragma unroll
         for (int w = 1; w < NW; ++w) {
-            lo += s_acc[w][at];
-            hi += s_acc[w][at + 16];
+            lo += s_acc[w][ei][at];
+            hi += s_acc[w][ei][at + 16];
         }
         cols.finish(a, et, lo, hi, sx, res);
     }
@@ -617,12 +629,20 @@ double rounds(long long tiles, int slots, double cost, double least)
     return cost * ((double)(tiles / slots) + (part > 0.0 ? least + (1.0 - least) * part : 0.0));
 }
 
-// Which kernel.  At most kStreamT tokens: the streaming kernel.  Then the 64 x 32 tiles (k in four
+// Which kernel.  At most kStreamT tokens: the streaming kernel, unless its blocks' reads of x, as many
+// bytes as of W at 16 tokens, are in the way (FP16, many outputs); with as many wavefronts as take the
+// steps of k in one round of loads, and 32 rows a block where that leaves a block a CU and k still is
+// one round (FP16 W of more than that streams at HBM's rate with 16 rows).  Then the 64 x 32 tiles (k in four
 // groups of wavefronts) while they fill no more than one round of the 256 CUs.  Then by the time of
 // the rounds, whose costs relative to 128 x 128 tiles with two blocks a CU are measured ones (FP16 72
 // us and e4m3 35 us a round at K 4096).  Measured (us, FP16 / e4m3; 128 x 128 with four stages (4)
 // and two (2)):
-//   16 x 2048 x 2048: stream 6.1 / 4.6, 64 x 32 tiles 8.1 / 5.7
+//   1 x 2048 x 1024: stream with 4 wavefronts 3.2 / 3.3, 8 3.8 / 3.7; K 2048: 5.6 / 3.6, 4.8 / 4.0
+//   16 x 5632 x 2048: 8 wavefronts, 16 rows 10.5 / 7.9, 32 rows 8.3 / 6.0; e4m3 4 wavefronts, 32 rows 5.4
+//   1 x 65536 x 2048: 8 wavefronts, 16 rows 51 / 44, 32 rows 61 / 35; e4m3 4 wavefronts, 32 rows 26
+//   16 x 2048 x 2048: stream 6.1 / 4.3, 64 x 32 tiles 8.1 / 5.5
+//   4, 8, 16 x 16384 x 4096 FP16: stream 28.6, 31.7, 38.2, 64 x 32 tiles 29.2, 29.3, 29.6
+//   4, 8, 16 x 65536 x 2048 FP16: stream 53.6, 60.1, 72.4, 64 x 32 tiles 61.4, 62.3, 63.5
 //   32 x 5632 x 2048: stream 13.2 / 9.3, 64 x 32 tiles 8.8 / 6.6
 //   256 x 2048 x 2048: 64 x 32 tiles 7.4 / 5.9, 64 x 64 9.1 / 6.5, 128 x 128 (4) 16.4 / 12.3
 //   256 x 5632 x 2048: 64 x 32 tiles 21.4 / 15.1, 64 x 64 13.5 / 9.0, 128 x 128 (4) 17.4 / 12.7
@@ -636,8 +656,17 @@ void launch(const LinearArgs &a, void *ws, hipStream_t s)
 {
     auto tiles = [&](int bn, int bt) { return (long long)((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt); };
     constexpr int LARGE = E4M3 ? 16 : 32;        // FP16 accumulators of 16 x 16 tiles do not stay in place
-    if (a.T <= kStreamT) {
-        hipLaunchKernelGGL((linear_stream_kernel<E4M3, 8>), dim3((unsigned int)((a.N + 15) / 16)), dim3(512), 0, s, a);
+    const int steps = (a.chunks + 7) / 8;
+    if (a.T <= kStreamT && (E4M3 || a.T <= 8 || a.N <= 8192 || steps <= 16)) {
+        auto stream = [&](auto nw, auto r) {
+            constexpr int NW = decltype(nw)::value, R = decltype(r)::value;
+            hipLaunchKernelGGL((linear_stream_kernel<E4M3, NW, R>), dim3((unsigned int)((a.N + 16 * R - 1) / (16 * R))),
+                               dim3(64 * NW), 0, s, a);
+        };
+        if (steps <= 16 && a.N <= 4096) stream(Const<4>{}, Const<1>{});
+        else if (steps <= 16) stream(Const<4>{}, Const<2>{});
+        else if (steps <= 32 && a.N > 4096 && (E4M3 || a.N <= 8192)) stream(Const<8>{}, Const<2>{});
+        else stream(Const<8>{}, Const<1>{});
         return;
     }
     if (tiles(64, 32) <= 256) return launch_tile<E4M3, 64, 32, 16, 2, 4>(a, splits_of(a, tiles(64, 32)), ws, s);
