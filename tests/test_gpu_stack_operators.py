@@ -179,3 +179,84 @@ def test_a_larger_batch_grows_the_buffers():
         q = torch.from_numpy(n["q"]).view(torch.float8_e4m3fn)
         got = dense.layer.run(q.to(DEV), dev(n["q_scale"]), residual=dev(x)).cpu().numpy()
         near(got, dense.output(q.double().numpy() * n["q_scale"].astype(np.float64)[:, None], x), f"T={T}")
+
+
+class Block:
+    """norm -> routed experts (scores) -> residual + norm to 8 bits -> dense layer, resident weights."""
+
+    def __init__(self, cfg, T, seed=0):
+        from w4a16_routed_expert_amd.layer import RoutedExpertLayer
+        g = np.random.default_rng(seed)
+        self.H, self.T = cfg.H, T
+        self.w = [dev((1.0 + 0.2 * g.standard_normal(cfg.H)).astype(np.float16)) for _ in range(2)]
+        self.lay = RoutedExpertLayer(cfg.H, cfg.I, cfg.E, cfg.k, dev(synth.make_expert_rows(cfg)),
+                                     dev(synth.make_router(cfg)), max_T=T, rule=rule())
+        self.dense = Dense(cfg.H, 320, True, seed).layer
+        f16 = dict(dtype=torch.float16, device=DEV)
+        self.n, self.y, self.s, self.out = (torch.empty((T, cfg.H), **f16) for _ in range(4))
+        self.q = torch.empty((T, cfg.H), dtype=torch.float8_e4m3fn, device=DEV)
+        self.scale = torch.empty(T, dtype=torch.float32, device=DEV)
+
+    def run(self, x, stream=None):
+        from w4a16_routed_expert_amd import binding as B
+        T, H = self.T, self.H
+        B.moe_residual_rmsnorm(x, None, self.w[0], EPS, T, H, norm=self.n, stream=stream)
+        self.lay.forward(self.n, self.y, stream)
+        B.moe_residual_rmsnorm(x, self.y, self.w[1], EPS, T, H, sum_out=self.s, q=self.q, q_scale=self.scale,
+                               stream=stream)
+        return self.dense.run(self.q, self.scale, residual=self.s, out=self.out, stream=stream)
+
+
+@pytest.mark.parametrize("T", [1, 24, 90])
+def test_a_block_captured_and_replayed(T):
+    cfg = synth.CONFIGS["tiny"]
+    b = Block(cfg, T)
+    xs = [dev(synth.make_x(cfg, T, step=s)) for s in range(4)]
+    want = [b.run(x).clone() for x in xs]
+    x = xs[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.run(x)
+    for i in (2, 0, 3, 1, 1):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(b.out, want[i]), f"replay on input {i}"
+        assert torch.equal(b.run(xs[i]), want[i]), "an eager call between replays"
+        torch.cuda.synchronize()
+
+
+def test_blocks_on_streams_of_their_own():
+    cfg = synth.CONFIGS["tiny"]
+    T = 40
+    blocks = [Block(cfg, T, seed=s) for s in range(2)]
+    xs = [dev(synth.make_x(cfg, T, step=s)) for s in range(2)]
+    want = [b.run(x).clone() for b, x in zip(blocks, xs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(8):
+        for b, x, s in zip(blocks, xs, streams):
+            b.out.zero_()
+            s.wait_stream(torch.cuda.current_stream())
+            b.run(x, s)
+        torch.cuda.synchronize()
+        for b, w in zip(blocks, want):
+            assert torch.equal(b.out, w)
+
+
+def test_buffers_that_grow_on_another_stream():
+    from w4a16_routed_expert_amd.layer import RoutedExpertLayer
+    cfg = synth.CONFIGS["tiny"]
+    rows, wr = dev(synth.make_expert_rows(cfg)), dev(synth.make_router(cfg))
+    lay = RoutedExpertLayer(cfg.H, cfg.I, cfg.E, cfg.k, rows, wr, max_T=1, rule=rule())
+    dense = Dense(cfg.H, 160, False, 3).layer
+    s = torch.cuda.Stream()
+    for T in (1, 30, 100, 400):
+        x = dev(synth.make_x(cfg, T, step=T))
+        want = lay.__class__(cfg.H, cfg.I, cfg.E, cfg.k, rows, wr, max_T=T, rule=rule()).forward(x)
+        ref = dense.run(x)
+        s.wait_stream(torch.cuda.current_stream())
+        y, d = lay.forward(x, stream=s), dense.run(x, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(d, ref)

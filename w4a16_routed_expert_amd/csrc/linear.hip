@@ -304,6 +304,14 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 // c ^ (r / 2 & 7), so the lanes that read one chunk of many rows spread over all
 // banks (a load's 64 lanes fill 1024 consecutive bytes of LDS: the swizzle is
 // in the addresses they read from).
+//   Bound by the matrix cores for large products, whose clock then falls (8192^3
+// FP16 832 us = 1.32 PFLOP/s, e4m3 410 us = 2.68; 8192 x 5632 x 4096 e4m3 182 us =
+// 2.08, 195 with bias and SiLU, whose two transcendental instructions a value
+// nothing overlaps; FP16 324 us = 1.17), by LDS with 128 x 128 tiles (64 KB read and
+// 32 KB written a step against 512 cycles of matrix instructions: 1333 x 2817 x
+// 2048 FP16 25 us).  Rows that do not start at multiples of 128 bytes cost a
+// second cache line a step (K 2064: 30 to 34 us); loading two steps of a row
+// together so that they share lines took 7 % off that and cost aligned rows 10 %.
 template <int OUTSTANDING>
 __device__ inline void arrive()
 {

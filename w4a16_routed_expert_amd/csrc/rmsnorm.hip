@@ -16,8 +16,10 @@
 // on every run and for every kernel shape.
 //
 // The row stays in registers between its one read and its writes: bound by
-// HBM for long batches, by one load round trip and the two reductions for
-// single rows.
+// HBM for long batches (8192 x 4096 with y and all outputs, 302 MB: 61.4 us =
+// 4.9 TB/s; a 1 GiB device copy moves 5.0 TB/s), by one load round trip and the
+// two reductions for single rows (1 x 2048 2.2 us, 32 x 2048 with 8-bit codes
+// 3.4 us).
 #include "moe_internal.h"
 
 namespace {

@@ -15,7 +15,7 @@
 // choice values and group values are in fp64, so a selection does not depend
 // on summation order or batch size.
 //
-// Small batches: one launch, a block per token and 16 experts; the block that
+// Small batches: one launch, a block per token and 8 experts; the block that
 // completes a token's logits selects its experts, the one that completes the
 // batch groups the pairs.  Larger ones: route_tile_kernel computes the logits of
 // 16 tokens with the fp64 matrix instruction (the experts divided among blocks
@@ -144,9 +144,13 @@ __device__ inline void select_wave(const ScoreRule &rule, int E, int k, int lane
 }
 
 // ------------------------------------------------------------ small batches: one launch
-constexpr int kScoredSmallT = 64;            // largest batch routed in one launch
-
-constexpr int kSmallE = 8;                   // experts per block of its logits
+// Bound by a chain of latencies: a load round trip, the sums, the logits handed
+// over at device scope, the selection, for more than one token the hand-over
+// to the block that groups.  H 2048, E 64, k 8: T = 1 7.8 us, T = 32 11.4 us.
+// Largest batch routed so (one thread a pair in the grouping): T = 64 12.5 us,
+// 15.9 by tiles; T = 17 9.7 and 15.8.
+constexpr int kScoredSmallT = 64;
+constexpr int kSmallE = 8;                   // experts per block of its logits (16: T = 1 9.3 us)
 
 union SmallLds {
     LogitsLds lg;
@@ -254,6 +258,12 @@ __global__ __launch_bounds__(kSelThreads) void route_scored_small_kernel(RouteAr
 // 16 wavefronts: the instruction's unit is shared with the conversions to fp64,
 // which four wavefronts a SIMD overlap better than two, and each then selects
 // for one token.
+//   T = 4096, H 2048, E 64: 30.8 us.  The products alone would take 14.7 us at the
+// 72 TFLOP/s of a large fp64 matrix product; of a block's 65 k cycles the loop
+// takes 54 k (33 k of matrix instructions; without the loop's loads 47 k, without
+// its conversions too 36 k) and the selection 8 k.  Weights moved to fp64 by
+// integer operations instead of conversions, packed sums of squares and other
+// orders of the steps between blocks left the loop at 55 k.
 constexpr int kTileT = 16;
 constexpr int kTileThreads = 1024;
 constexpr int kTileWaves = kTileThreads / 64;
@@ -585,7 +595,9 @@ __global__ __launch_bounds__(kPlaceWaves * 64) void route_place_kernel(RouteArgs
 }
 
 // Tiles whose experts are divided among blocks: enough blocks for the GPU's
-// 256 CUs.
+// 256 CUs.  Measured with 16, 32, 64 experts a block (H 2048, E 64, whole call,
+// us): T = 512 16.9, 21.7, 30.9; T = 1024 18.2, 22.2, 31.2; T = 2048 28.4, 23.5,
+// 31.7; T = 4096 with 64 34.1.
 constexpr int kSplitTiles = 128;
 
 // Workspace: the counters (zero between calls), then the logits handed between
@@ -705,7 +717,9 @@ int moe_route_scored(const void *x_dev, const void *w_router_dev, const float *s
     else launch_tiles<1>(a, r, counts, done, s);
     rc = moe::check_launch("moe_route_scored (select)");
     if (rc) return rc;
-    // at least 4 tiles per block, and at most 256 blocks: every block reads all tiles' counts
+    // at least 4 tiles per block, and at most 256 blocks: every block reads all tiles' counts.  Whole call
+    // with 1, 2, 4, 8, 16 tiles a block (H 128, us): T = 512 10.2, 10.3, 10.3, 10.3, 11.1; T = 16384 48.7,
+    // 40.1, 36.4, 35.8, 37.2; T = 65536 336, 227, 171, 142, 131
     const int tiles = tiles_total > 1024 ? (tiles_total + 255) / 256 : 4;
     hipLaunchKernelGGL(route_place_kernel, dim3((unsigned int)((tiles_total + tiles - 1) / tiles)),
                        dim3(kPlaceWaves * 64), 0, s, a, (const int *)counts, tiles_total, tiles);

@@ -7,6 +7,8 @@ its own: torch provides memory and streams, the HIP library does the work.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import binding as B
@@ -81,11 +83,15 @@ class RoutedExpertLayer:
 
     def route(self, x: torch.Tensor, stream=None, exact: bool = False):
         T = x.shape[0]
+        if self.rule is not None and exact:
+            raise ValueError("the integer routing path has no scores")
         if T > self.max_T:
-            self._alloc(T)
+            if self.rule is None:
+                self._alloc(T)
+            else:                                    # the new workspace's zeros are written on the current stream
+                with _ordered(stream):
+                    self._alloc(T)
         if self.rule is not None:
-            if exact:
-                raise ValueError("the integer routing path has no scores")
             B.moe_route_scored(x, self.router, self.select_bias, T, self.H, self.E, self.k, self.rule, self.logits,
                                self.topk_ids, self.topk_w, self.expert_offsets, self.sorted_pairs, self.pair_pos,
                                self.active_list, self.n_active, self.scored_ws, self.scored_ws.numel(), stream)
@@ -266,6 +272,16 @@ class RoutedExpertLayer:
                              if st == B.MOE_ERR_ABSENT_EXPERT else "expert FFN status word set")
 
 
+@contextlib.contextmanager
+def _ordered(stream):
+    """New buffers for work on `stream`: what the current stream does with their memory comes after the
+    work that `stream` has, and before what it gets next."""
+    cur, s = torch.cuda.current_stream(), _torch_stream(stream)
+    cur.wait_stream(s)
+    yield
+    s.wait_stream(cur)
+
+
 def _torch_stream(stream):
     """A torch stream object for None (the current stream), a torch stream or a raw handle."""
     if stream is None:
@@ -410,12 +426,14 @@ class DenseFFN:
 
     w_up: CUDA tensor [I, H], float16, or float8_e4m3fn with up_scale (float32 [I]): the layer then
     takes 8-bit activations with their scales (moe_residual_rmsnorm's q and q_scale).  w_down:
-    float16 [H, I].  up_bias, down_bias: float32 or None.  act: a binding MOE_ACT_* value.
+    float16 [H, I].  up_bias, down_bias: float32 or None.  act: a binding MOE_ACT_* value.  Calls use
+    one set of buffers (one stream at a time); a batch above max_T replaces them, so a captured graph
+    needs max_T set to its batch.
     """
 
     def __init__(self, w_up: torch.Tensor, w_down: torch.Tensor, up_scale: torch.Tensor | None = None,
                  up_bias: torch.Tensor | None = None, down_bias: torch.Tensor | None = None,
-                 act: int = B.MOE_ACT_SILU, device: str | torch.device = "cuda:0"):
+                 act: int = B.MOE_ACT_SILU, max_T: int = 64, device: str | torch.device = "cuda:0"):
         self.I, self.H = w_up.shape
         self.e4m3 = w_up.dtype == torch.float8_e4m3fn
         if not self.e4m3 and w_up.dtype != torch.float16 or w_down.dtype != torch.float16:
@@ -425,11 +443,9 @@ class DenseFFN:
         self.w_up, self.w_down, self.up_scale = w_up, w_down, up_scale
         self.up_bias, self.down_bias, self.act = up_bias, down_bias, act
         self.device = torch.device(device)
-        self.max_T = -1
+        self._alloc(max_T)
 
-    def _ensure(self, T: int):
-        if T <= self.max_T:
-            return
+    def _alloc(self, T: int):
         self.max_T = T
         self.h = torch.empty((max(T, 1), self.I), dtype=torch.float16, device=self.device)
         up = B.MOE_LINEAR_E4M3 if self.e4m3 else B.MOE_LINEAR_FP16
@@ -441,7 +457,9 @@ class DenseFFN:
             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x: float16 [T, H], or the 8-bit activations with x_scale (float32 [T])."""
         T = x.shape[0]
-        self._ensure(T)
+        if T > self.max_T:
+            with _ordered(stream):
+                self._alloc(T)
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.float16, device=self.device)
         n = self.ws.numel()
