@@ -290,9 +290,11 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 // ------------------------------------------------------------ many tokens
 // Block tile BN outputs x BT tokens by 4 wavefronts, 2 x 2, each BN/2 x BT/2 in
 // registers (or KG such groups of 4, each taking every KG-th step of k, whose
-// sums meet in LDS: for tiles too few to fill the GPU); 128 bytes of k a step.  A step's operands lie in LDS in three
-// parts: the tokens X, and the first and second half (WA, WB) of every
-// wavefront's output rows, for B steps at once.  Per step:
+// sums meet in LDS: for tiles too few to fill the GPU, and to have two
+// wavefronts a SIMD where one block fills a CU's LDS); 128 bytes of k a step.
+// A step's operands lie in LDS in three parts: the tokens X, and the first and
+// second half (WA, WB) of every wavefront's output rows, for B steps at once.
+// Per step:
 //     barrier; ask for WB of step k + B - 1; read WB(k); multiply WA(k) . X(k)
 //     barrier; ask for X, WA of step k + B; read X, WA of step k + 1; multiply WB(k) . X(k)
 // A part is overwritten after the barrier that follows the products it was
@@ -309,9 +311,9 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 // 2.08, 195 with bias and SiLU, whose two transcendental instructions a value
 // nothing overlaps; FP16 324 us = 1.17), by LDS with 128 x 128 tiles (64 KB read and
 // 32 KB written a step against 512 cycles of matrix instructions: 1333 x 2817 x
-// 2048 FP16 25 us).  Rows that do not start at multiples of 128 bytes cost a
-// second cache line a step (K 2064: 30 to 34 us); loading two steps of a row
-// together so that they share lines took 7 % off that and cost aligned rows 10 %.
+// 2048 FP16 24 us).  Rows that do not start at multiples of 128 bytes cost a
+// second cache line a step (K 2064: 29 us); loading two steps of a row together so
+// that they share lines took 7 % off that and cost aligned rows 10 %.
 template <int OUTSTANDING>
 __device__ inline void arrive()
 {
@@ -479,11 +481,11 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     }
     arrive<0>();                                                 // no load is on its way to LDS any more
 
-    if constexpr (KG > 1) {
+    if constexpr (KG == 4) {
         // the groups' sums meet in LDS, [group][token][output], two groups a
         // stage of X; then a lane finishes 8 outputs of a token
         constexpr int ROW = BN / 4, ITEMS = BT * BN / 8;         // 4-output chunks of a token; lanes of work
-        static_assert(KG == 4 && MT == 16 && 2 * BT * ROW <= KG * BT * 8, "two groups' sums fit a stage");
+        static_assert(MT == 16 && 2 * BT * ROW <= KG * BT * 8, "two groups' sums fit a stage");
         i32x4 *const x0 = part<E4M3, BN, BT, MT, KG, 0, 0>(), *const x1 = part<E4M3, BN, BT, MT, KG, 1, 0>();
         i32x4 *mine = (grp & 2 ? x1 : x0) + (grp & 1) * (BT * ROW);
 #pragma unroll
@@ -511,16 +513,49 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
         }
         return;
     } else {
+    constexpr int NH = KG == 2 ? 1 : 2;                          // halves of its output rows a wavefront finishes
+    if constexpr (KG == 2) {
+        // group g finishes half g of its wavefronts' output rows (in acc[0] from here): it hands the
+        // other's sums over and adds what it gets
+        constexpr int CH = MT * MT / 256;                        // 16-byte chunks of a tile's sums in a lane
+        static_assert(4 * 64 * FT * HN * CH <= KG * BT * 8, "a group's half of the sums fits a stage of X");
+        i32x4 *const x0 = part<E4M3, BN, BT, MT, KG, 0, 0>(), *const x1 = part<E4M3, BN, BT, MT, KG, 1, 0>();
+        i32x4 *const give = (grp ? x1 : x0) + wave * (64 * FT * HN * CH) + lane;
+        const i32x4 *const get = (grp ? x0 : x1) + wave * (64 * FT * HN * CH) + lane;
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+#pragma unroll
+            for (int i = 0; i < HN; ++i) {
+                const typename S::Acc v = grp ? acc[0][j][i] : acc[1][j][i];
+                acc[0][j][i] = grp ? acc[1][j][i] : acc[0][j][i];
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+                    give[((j * HN + i) * CH + c) * 64] =
+                        __builtin_bit_cast(i32x4, f32x4{v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]});
+            }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < FT; ++j)
+#pragma unroll
+            for (int i = 0; i < HN; ++i)
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const f32x4 v = __builtin_bit_cast(f32x4, get[((j * HN + i) * CH + c) * 64]);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) acc[0][j][i][4 * c + b] += v[b];
+                }
+        __syncthreads();                                         // the same LDS serves the epilogue
+    }
     // Epilogue: the sums pass through LDS, 2 x 16 tokens of a wavefront at a
     // time, so that a lane finishes 8 neighbouring outputs of a token.
-    constexpr int CW = BN / 8;                                   // 4-output chunks of a wavefront's row
+    constexpr int CW = BN / 16 * NH;                             // 4-output chunks of a wavefront's row
     constexpr int PT = 32 / MT;                                  // token tiles at a time
     static_assert(32 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
     i32x4 *mine = ((wave & 2) ? (part<E4M3, BN, BT, MT, KG, 1, 0>() + grp * (BT * 8)) : (part<E4M3, BN, BT, MT, KG, 0, 0>() + grp * (BT * 8))) + (wave & 1) * (32 * CW);
     constexpr int LPT = CW / 2, TPI = 64 / LPT;                  // lanes a token, tokens at once
     Columns<E4M3> cols;
     const int lane_n = lane % LPT;
-    cols.load(a, n0 + (wave >> 1) * (BN / 2) + 8 * lane_n);
+    cols.load(a, n0 + (wave >> 1) * (BN / 2) + (KG == 2 ? grp * (BN / 4) : 0) + 8 * lane_n);
     const int t_wave = (wave & 1) * (BT / 2);
 #pragma unroll 1
     for (int p = 0; p < FT / PT; ++p) {
@@ -530,7 +565,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
             for (int u = 0; u < PT; ++u)
 #pragma unroll
-                for (int i = 0; i < 2 * HN; ++i)
+                for (int i = 0; i < NH * HN; ++i)
 #pragma unroll
                     for (int c = 0; c < MT / 16 * MT / 16; ++c) {
                         const typename S::Acc v = acc[i / HN][q * PT + u][i % HN];
@@ -643,8 +678,8 @@ double rounds(long long tiles, int slots, double cost, double least)
 // one round (FP16 W of more than that streams at HBM's rate with 16 rows).  Then the 64 x 32 tiles (k in four
 // groups of wavefronts) while they fill no more than one round of the 256 CUs.  Then by the time of
 // the rounds, whose costs relative to 128 x 128 tiles with two blocks a CU are measured ones (FP16 72
-// us and e4m3 35 us a round at K 4096).  Measured (us, FP16 / e4m3; 128 x 128 with four stages (4)
-// and two (2)):
+// us and e4m3 35 us a round at K 4096).  Measured (us, FP16 / e4m3; 128 x 128 with two groups of
+// wavefronts (g) and two blocks a CU (b)):
 //   1 x 2048 x 1024: stream with 4 wavefronts 3.2 / 3.3, 8 3.8 / 3.7; K 2048: 5.6 / 3.6, 4.8 / 4.0
 //   16 x 5632 x 2048: 8 wavefronts, 16 rows 10.5 / 7.9, 32 rows 8.3 / 6.0; e4m3 4 wavefronts, 32 rows 5.4
 //   1 x 65536 x 2048: 8 wavefronts, 16 rows 51 / 44, 32 rows 61 / 35; e4m3 4 wavefronts, 32 rows 26
@@ -652,18 +687,21 @@ double rounds(long long tiles, int slots, double cost, double least)
 //   4, 8, 16 x 16384 x 4096 FP16: stream 28.6, 31.7, 38.2, 64 x 32 tiles 29.2, 29.3, 29.6
 //   4, 8, 16 x 65536 x 2048 FP16: stream 53.6, 60.1, 72.4, 64 x 32 tiles 61.4, 62.3, 63.5
 //   32 x 5632 x 2048: stream 13.2 / 9.3, 64 x 32 tiles 8.8 / 6.6
-//   256 x 2048 x 2048: 64 x 32 tiles 7.4 / 5.9, 64 x 64 9.1 / 6.5, 128 x 128 (4) 16.4 / 12.3
-//   256 x 5632 x 2048: 64 x 32 tiles 21.4 / 15.1, 64 x 64 13.5 / 9.0, 128 x 128 (4) 17.4 / 12.7
-//   512 x 5632 x 4096: 64 x 64 45 / 25, 128 x 128 (4) 35 / 22, (2) 41 / 25, 256 x 256 79 / 55
-//   2048 x 4096 x 4096: 128 x 128 (4) 81 / 45, (2) 72 / 36, 256 x 256 89 / 57
-//   2048 x 5632 x 4096: 128 x 128 (4) 125 / 65, (2) 127 / 58, 256 x 256 101 / 60
-//   4096 x 4096 x 4096: 128 x 128 (2) 145 / 70, 256 x 256 127 / 67
-//   70 x 65536 x 2048: 64 x 64 82 / 47, 128 x 128 (2) 74 / 34, 256 x 256 84 / 46
+//   256 x 2048 x 2048: 64 x 32 tiles 7.4 / 5.9, 64 x 64 9.1 / 6.5
+//   256 x 5632 x 2048: 64 x 32 tiles 21 / 15, 64 x 64 15 / 9.9, 128 x 128 (g) 19 / 13
+//   512 x 5632 x 4096: 64 x 64 45 / 25, 128 x 128 (g) 33 / 20, (b) 41 / 25, 256 x 256 79 / 55
+//   1333 x 2817 x 2064: 64 x 64 40 / 25, 128 x 128 (g) 29 / 18, (b) 33 / 20, 256 x 256 56 / 43
+//   2048 x 4096 x 4096: 128 x 128 (g) 79 / 43, (b) 74 / 38, 256 x 256 92 / 58
+//   2048 x 5632 x 4096: 128 x 128 (g) 112 / 61, (b) 117 / 59, 256 x 256 107 / 60
+//   4096 x 4096 x 4096: 128 x 128 (g) 159 / 83, (b) 144 / 75, 256 x 256 138 / 70
+//   70 x 65536 x 2048: 64 x 64 82 / 47, 128 x 128 (b) 74 / 34, 256 x 256 84 / 46
+// 128 x 128 tiles in FP16 with 32 x 32 instructions: (g) 30 and (b) 34 at 1333 x 2817 x 2064; 256 x 256
+// ones with 16 x 16 instructions 78 there and 152 at 4096 x 4096 x 4096, as their accumulators do not
+// stay in place.  With four stages instead of two groups a 128 x 128 tile took 33 / 19.
 template <bool E4M3>
 void launch(const LinearArgs &a, void *ws, hipStream_t s)
 {
     auto tiles = [&](int bn, int bt) { return (long long)((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt); };
-    constexpr int LARGE = E4M3 ? 16 : 32;        // FP16 accumulators of 16 x 16 tiles do not stay in place
     const int steps = (a.chunks + 7) / 8;
     if (a.T <= kStreamT && (E4M3 || a.T <= 8 || a.N <= 8192 || steps <= 16)) {
         auto stream = [&](auto nw, auto r) {
@@ -682,9 +720,9 @@ void launch(const LinearArgs &a, void *ws, hipStream_t s)
     const double two = rounds(tiles(128, 128), 512, 1.0, 0.5), large = rounds(tiles(256, 256), 256, E4M3 ? 1.87 : 1.75, 0.65);
     const double best = std::min(std::min(small, deep), std::min(two, large));
     if (small == best) return launch_tile<E4M3, 64, 64, 16, 4>(a, 1, ws, s);
-    if (deep == best) return launch_tile<E4M3, 128, 128, LARGE, 4>(a, 1, ws, s);
-    if (two == best) return launch_tile<E4M3, 128, 128, LARGE, 2>(a, 1, ws, s);
-    launch_tile<E4M3, 256, 256, LARGE, 2>(a, 1, ws, s);
+    if (deep == best) return launch_tile<E4M3, 128, 128, 16, 2, 2>(a, 1, ws, s);
+    if (two == best) return launch_tile<E4M3, 128, 128, 16, 2>(a, 1, ws, s);
+    launch_tile<E4M3, 256, 256, E4M3 ? 16 : 32, 2>(a, 1, ws, s);
 }
 
 constexpr int kMaxLd = 1 << 22;                  // elements: 256 rows stay within 32-bit offsets
