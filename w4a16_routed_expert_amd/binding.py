@@ -241,14 +241,18 @@ def _current_stream() -> int:
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
-def _device(t) -> int:
-    """Ordinal of a GPU tensor's device (-1: an address or nothing, taken as the current device's)."""
+def _begin(t, stream):
+    """(device ordinal of a call's first argument, handle of its stream): ordinal -1 for an address or
+    nothing, which is taken as the current device's; no handle if the device is not the current one."""
     if t is None or isinstance(t, int):
-        return -1
+        return -1, _s(stream)
     d = t.get_device()
     if d < 0:
         raise ValueError("a tensor is not in GPU memory")
-    return d
+    c = _torch_c or _c()
+    if d != c._cuda_getDevice():
+        return d, None
+    return d, c._cuda_getCurrentRawStream(d) if stream is None else _s(stream)
 
 
 def _g(t, dev: int):
@@ -261,15 +265,10 @@ def _g(t, dev: int):
     return t.data_ptr()
 
 
-def _elsewhere(d: int) -> bool:
-    """Whether tensors of device d (_device) are on another device than the current one."""
-    return d >= 0 and d != _c()._cuda_getDevice()
-
-
 def _there(d: int, call, args: dict):
     """`call` with device d current, so that its stream and launches are that device's."""
     import torch
-    del args["d"]
+    del args["d"], args["s"]
     with torch.cuda.device(d):
         return call(**args)
 
@@ -337,13 +336,13 @@ def route_rule(score=MOE_SCORE_SOFTMAX, n_group=1, topk_group=1, group_score=MOE
 
 def moe_route_scored(x, w_router, select_bias, T, H, E, k, rule: RouteRule, logits, topk_ids, topk_w, expert_offsets,
                      sorted_pairs, pair_pos, active_list, n_active, ws, ws_bytes, stream=None):
-    d = _device(x)
-    if _elsewhere(d):
+    d, s = _begin(x, stream)
+    if s is None:
         return _there(d, moe_route_scored, locals())
     _check(load().moe_route_scored(_g(x, d), _g(w_router, d), _g(select_bias, d), T, H, E, k,
                                    None if rule is None else ctypes.byref(rule), _g(logits, d), _g(topk_ids, d),
                                    _g(topk_w, d), _g(expert_offsets, d), _g(sorted_pairs, d), _g(pair_pos, d),
-                                   _g(active_list, d), _g(n_active, d), _g(ws, d), ws_bytes, _s(stream)))
+                                   _g(active_list, d), _g(n_active, d), _g(ws, d), ws_bytes, s))
 
 
 def moe_w4a16_gateup(x, T, H, I, E, k, rows, row_stride, slot_map, expert_offsets, sorted_pairs, active_list,
@@ -460,12 +459,12 @@ def _ld(t, ld, width):
 def moe_residual_rmsnorm(x, y, w, eps, T, H, sum_out=None, norm=None, q=None, q_scale=None, ldx=None, ldy=None,
                          ld_sum=None, ld_norm=None, ldq=None, stream=None):
     """Row strides (elements) are those of 2-D tensors unless given."""
-    d = _device(x)
-    if _elsewhere(d):
+    d, s = _begin(x, stream)
+    if s is None:
         return _there(d, moe_residual_rmsnorm, locals())
     _check(load().moe_residual_rmsnorm(_g(x, d), _ld(x, ldx, H), _g(y, d), _ld(y, ldy, H), _g(w, d), eps, T, H,
                                        _g(sum_out, d), _ld(sum_out, ld_sum, H), _g(norm, d), _ld(norm, ld_norm, H),
-                                       _g(q, d), _ld(q, ldq, H), _g(q_scale, d), _s(stream)))
+                                       _g(q, d), _ld(q, ldq, H), _g(q_scale, d), s))
 
 
 def moe_linear_workspace_size(T: int, N: int, K: int, type: int) -> int:
@@ -475,12 +474,12 @@ def moe_linear_workspace_size(T: int, N: int, K: int, type: int) -> int:
 def moe_linear(x, w, T, N, K, type, y, x_scale=None, w_scale=None, bias=None, act=MOE_ACT_NONE, residual=None,
                ws=None, ws_bytes=0, ldx=None, ldw=None, ldr=None, ldy=None, stream=None):
     """Row strides (elements) are those of 2-D tensors unless given."""
-    d = _device(x)
-    if _elsewhere(d):
+    d, s = _begin(x, stream)
+    if s is None:
         return _there(d, moe_linear, locals())
     _check(load().moe_linear(_g(x, d), _ld(x, ldx, K), _g(x_scale, d), _g(w, d), _ld(w, ldw, K), _g(w_scale, d),
                              _g(bias, d), _g(residual, d), _ld(residual, ldr, N), T, N, K, type, act, _g(y, d),
-                             _ld(y, ldy, N), _g(ws, d), ws_bytes, _s(stream)))
+                             _ld(y, ldy, N), _g(ws, d), ws_bytes, s))
 
 
 # ------------------------------------------------------------------ resident expert table
