@@ -39,10 +39,10 @@ def test_rmsnorm_refusals():
     norm(T=0, x=None, y=None, w=None)                # nothing to do
 
 
-def scored(T=4, H=256, E=8, k=2, x=F, wr=F, ids=F, ws=F, ws_bytes=1 << 20, rule="default", **r):
+def scored(T=4, H=256, E=8, k=2, x=F, wr=F, ids=F, ws=F, ws_bytes=1 << 20, rule="default", bias=None, **r):
     if rule == "default":
         rule = B.route_rule(**r)
-    B.moe_route_scored(x, wr, None, T, H, E, k, rule, None, ids, F, F, F, F, F, F, ws, ws_bytes, stream=0)
+    B.moe_route_scored(x, wr, bias, T, H, E, k, rule, None, ids, F, F, F, F, F, F, ws, ws_bytes, stream=0)
 
 
 def test_scored_routing_refusals():
@@ -50,6 +50,8 @@ def test_scored_routing_refusals():
                dict(H=4224)):
         refused(lambda: scored(**kw), B.MOE_ERR_UNSUPPORTED, "=")
     refused(lambda: scored(rule=None), B.MOE_ERR_INVALID_ARG, "rule")
+    refused(lambda: scored(bias=F + 2), B.MOE_ERR_INVALID_ARG, "aligned")
+    refused(lambda: scored(x=F + 8), B.MOE_ERR_INVALID_ARG, "aligned")
     for kw, word in ((dict(score=2), "score"), (dict(score=-1), "score"), (dict(group_score=2), "group score"),
                      (dict(n_group=3), "n_group"), (dict(n_group=0), "n_group"), (dict(n_group=16), "n_group"),
                      (dict(n_group=4, topk_group=5), "topk_group"), (dict(n_group=4, topk_group=0), "topk_group"),
