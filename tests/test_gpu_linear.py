@@ -242,3 +242,11 @@ def test_few_tokens_and_many_outputs(T, N, K, type):
     c = Case(T, N, K, type, whole=True)
     c.check_whole(c.run(), f"{T}x{N}x{K}")
     c.check_whole(c.run(ldx=K + 16, ldw=K + 48, ldy=N + 3, offset=1), f"{T}x{N}x{K} strided")
+
+
+@pytest.mark.parametrize("type", [FP16, E4M3], ids=["fp16", "e4m3"])
+def test_many_tokens_and_outputs_with_a_long_sum(type):
+    c = Case(3990, 3993, 4112, type, whole=True)
+    c.check_whole(c.run(), "3990x3993x4112")
+    c = Case(3990, 3985, 4112, type, whole=False)
+    c.check(c.run(SILU), SILU, "3990x3985x4112 silu")

@@ -675,11 +675,11 @@ double rounds(long long tiles, int slots, double cost, double least)
 // Which kernel.  At most kStreamT tokens: the streaming kernel, unless its blocks' reads of x, as many
 // bytes as of W at 16 tokens, are in the way (FP16, many outputs); with as many wavefronts as take the
 // steps of k in one round of loads, and 32 rows a block where that leaves a block a CU and k still is
-// one round (FP16 W of more than that streams at HBM's rate with 16 rows).  Then the 64 x 32 tiles (k in four
-// groups of wavefronts) while they fill no more than one round of the 256 CUs.  Then by the time of
-// the rounds, whose costs relative to 128 x 128 tiles with two blocks a CU are measured ones (FP16 72
-// us and e4m3 35 us a round at K 4096).  Measured (us, FP16 / e4m3; 128 x 128 with two groups of
-// wavefronts (g) and two blocks a CU (b)):
+// one round (FP16 W of more than that streams at HBM's rate with 16 rows).  Then the 64 x 32 tiles (k
+// in four groups of wavefronts) while they fill no more than one round of the 256 CUs.  Then by the time
+// of the rounds, whose costs relative to 128 x 128 tiles with two blocks a CU are measured ones (FP16 72
+// us and e4m3 35 us a round at K 4096; a 256 x 256 tile's start and end weigh more when k is short).
+// Measured (us, FP16 / e4m3; 128 x 128 with two groups of wavefronts (g) and two blocks a CU (b)):
 //   1 x 2048 x 1024: stream with 4 wavefronts 3.2 / 3.3, 8 3.8 / 3.7; K 2048: 5.6 / 3.6, 4.8 / 4.0
 //   16 x 5632 x 2048: 8 wavefronts, 16 rows 10.5 / 7.9, 32 rows 8.3 / 6.0; e4m3 4 wavefronts, 32 rows 5.4
 //   1 x 65536 x 2048: 8 wavefronts, 16 rows 51 / 44, 32 rows 61 / 35; e4m3 4 wavefronts, 32 rows 26
@@ -694,6 +694,7 @@ double rounds(long long tiles, int slots, double cost, double least)
 //   2048 x 4096 x 4096: 128 x 128 (g) 79 / 43, (b) 74 / 38, 256 x 256 92 / 58
 //   2048 x 5632 x 4096: 128 x 128 (g) 112 / 61, (b) 117 / 59, 256 x 256 107 / 60
 //   4096 x 4096 x 4096: 128 x 128 (g) 159 / 83, (b) 144 / 75, 256 x 256 138 / 70
+//   4096 x 4096 x 1024: 128 x 128 (g) 51 / 36, (b) 43 / 31, 256 x 256 45 / 36
 //   70 x 65536 x 2048: 64 x 64 82 / 47, 128 x 128 (b) 74 / 34, 256 x 256 84 / 46
 // 128 x 128 tiles in FP16 with 32 x 32 instructions: (g) 30 and (b) 34 at 1333 x 2817 x 2064; 256 x 256
 // ones with 16 x 16 instructions 78 there and 152 at 4096 x 4096 x 4096, as their accumulators do not
@@ -717,7 +718,8 @@ void launch(const LinearArgs &a, void *ws, hipStream_t s)
     }
     if (tiles(64, 32) <= 256) return launch_tile<E4M3, 64, 32, 16, 2, 4>(a, splits_of(a, tiles(64, 32)), ws, s);
     const double small = rounds(tiles(64, 64), 512, 0.45, 0.5), deep = rounds(tiles(128, 128), 256, 0.6, 0.5);
-    const double two = rounds(tiles(128, 128), 512, 1.0, 0.5), large = rounds(tiles(256, 256), 256, E4M3 ? 1.87 : 1.75, 0.65);
+    const double two = rounds(tiles(128, 128), 512, 1.0, 0.5);
+    const double large = rounds(tiles(256, 256), 256, 1.64 * (steps + 14) / (steps + 7), 0.65);
     const double best = std::min(std::min(small, deep), std::min(two, large));
     if (small == best) return launch_tile<E4M3, 64, 64, 16, 4>(a, 1, ws, s);
     if (deep == best) return launch_tile<E4M3, 128, 128, 16, 2, 2>(a, 1, ws, s);
