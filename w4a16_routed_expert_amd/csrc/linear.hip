@@ -84,10 +84,12 @@ struct Columns {
         m = min(8, a.N - n);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-            const int c = min(n + r, a.N - 1);
-            scale[r] = E4M3 ? a.w_scale[c] : 1.0f;
-            bias[r] = a.bias ? a.bias[c] : 0.0f;
+            scale[r] = E4M3 ? a.w_scale[min(n + r, a.N - 1)] : 1.0f;
+            bias[r] = 0.0f;
         }
+        if (!a.bias) return;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) bias[r] = a.bias[min(n + r, a.N - 1)];
     }
 
     __device__ inline half8 residual(const LinearArgs &a, int t) const
@@ -113,43 +115,58 @@ struct Columns {
         o[1] = hi;
     }
 
-    // The 8 outputs of token t from their sums (lo, hi), the token's scale and
-    // residuals.
-    __device__ inline void finish(const LinearArgs &a, int t, f32x4 lo, f32x4 hi, float sx, half8 res) const
+    // The 8 outputs of tokens t[0 .. U) from their sums (lo, hi), the tokens' scales and residuals.
+    template <int U>
+    __device__ inline void finish(const LinearArgs &a, const int (&t)[U], const f32x4 (&lo)[U], const f32x4 (&hi)[U],
+                                  const float (&sx)[U], const half8 (&res)[U]) const
     {
-        float v[8];
+        float v[U][8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            v[r] = lo[r];
-            v[4 + r] = hi[r];
-        }
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int r = 0; r < 8; ++r) v[r] = E4M3 ? fmaf(v[r], sx * scale[r], bias[r]) : v[r] + bias[r];
+            for (int r = 0; r < 8; ++r) {
+                const float s = r < 4 ? lo[u][r] : hi[u][r - 4];
+                v[u][r] = E4M3 ? fmaf(s, sx[u] * scale[r], bias[r]) : s + bias[r];
+            }
         if (a.act == MOE_ACT_SILU) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) v[r] = gate(v[r], v[r]);
+            for (int i = 0; i < 8 * U; ++i) v[i / 8][i % 8] = gate(v[i / 8][i % 8], v[i / 8][i % 8]);
         } else if (a.act == MOE_ACT_GELU) {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) v[r] = gelu(v[r]);
+            for (int i = 0; i < 8 * U; ++i) v[i / 8][i % 8] = gelu(v[i / 8][i % 8]);
         } else if (a.act == MOE_ACT_GELU_TANH) {
             // 0.5 v (1 + tanh u) = v / (1 + exp(-2u)), u = sqrt(2/pi) (v + 0.044715 v^3)
 #pragma unroll
-            for (int r = 0; r < 8; ++r) v[r] = gate(v[r], v[r] * fmaf(0.07135481627f * v[r], v[r], 1.5957691216f));
-        }
-        half8 o;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) o[r] = (_Float16)(v[r] + (float)res[r]);
-        if (t >= a.T || m <= 0) return;
-        uint16_t *y = a.y + (long long)t * a.ldy + n;
-        if (m == 8) {
-            reinterpret_cast<Out8 *>(y)->v = o;
-        } else {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const _Float16 h = o[r];
-                if (r < m) y[r] = __builtin_bit_cast(uint16_t, h);
+            for (int i = 0; i < 8 * U; ++i) {
+                const float w = v[i / 8][i % 8];
+                v[i / 8][i % 8] = gate(w, w * fmaf(0.07135481627f * w, w, 1.5957691216f));
             }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            half8 o;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) o[r] = (_Float16)(v[u][r] + (float)res[u][r]);
+            if (t[u] >= a.T || m <= 0) continue;
+            uint16_t *y = a.y + (long long)t[u] * a.ldy + n;
+            if (m == 8) {
+                reinterpret_cast<Out8 *>(y)->v = o;
+            } else {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const _Float16 h = o[r];
+                    if (r < m) y[r] = __builtin_bit_cast(uint16_t, h);
+                }
+            }
+        }
+    }
+    __device__ inline void finish(const LinearArgs &a, int t, f32x4 lo, f32x4 hi, float sx, half8 res) const
+    {
+        const int ts[1] = {t};
+        const f32x4 los[1] = {lo}, his[1] = {hi};
+        const float sxs[1] = {sx};
+        const half8 ress[1] = {res};
+        finish<1>(a, ts, los, his, sxs, ress);
     }
 };
 
@@ -330,6 +347,8 @@ __device__ inline i32x4 *part()
     return s;
 }
 
+constexpr int kNoLoads = 0x0F70;                                 // s_waitcnt operand: vmcnt(0)
+
 template <int V>
 struct Const {
     static constexpr int value = V;
@@ -479,7 +498,14 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
             }
         }
     }
-    arrive<0>();                                                 // no load is on its way to LDS any more
+    constexpr int NH = KG == 2 ? 1 : 2;                          // halves of its output rows a wavefront finishes
+    constexpr int CW = BN / 16 * NH, LPT = CW / 2;               // 4-output chunks of its row; lanes that finish a token
+    Columns<E4M3> cols;
+    if constexpr (KG != 4) cols.load(a, n0 + (wave >> 1) * (BN / 2) + (KG == 2 ? grp * (BN / 4) : 0) + lane % LPT * 8);
+    // No load is on its way to LDS any more.  The builtin tells the compiler, which would else wait for
+    // memory (and so for the stores before) at every use of LDS below.
+    __builtin_amdgcn_s_waitcnt(kNoLoads);
+    arrive<0>();
 
     if constexpr (KG == 4) {
         // the groups' sums meet in LDS, [group][token][output], two groups a
@@ -513,7 +539,6 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
         }
         return;
     } else {
-    constexpr int NH = KG == 2 ? 1 : 2;                          // halves of its output rows a wavefront finishes
     if constexpr (KG == 2) {
         // group g finishes half g of its wavefronts' output rows (in acc[0] from here): it hands the
         // other's sums over and adds what it gets
@@ -548,14 +573,11 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     }
     // Epilogue: the sums pass through LDS, 2 x 16 tokens of a wavefront at a
     // time, so that a lane finishes 8 neighbouring outputs of a token.
-    constexpr int CW = BN / 16 * NH;                             // 4-output chunks of a wavefront's row
     constexpr int PT = 32 / MT;                                  // token tiles at a time
     static_assert(32 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
     i32x4 *mine = ((wave & 2) ? (part<E4M3, BN, BT, MT, KG, 1, 0>() + grp * (BT * 8)) : (part<E4M3, BN, BT, MT, KG, 0, 0>() + grp * (BT * 8))) + (wave & 1) * (32 * CW);
-    constexpr int LPT = CW / 2, TPI = 64 / LPT;                  // lanes a token, tokens at once
-    Columns<E4M3> cols;
+    constexpr int TPI = 64 / LPT;                                // tokens at once
     const int lane_n = lane % LPT;
-    cols.load(a, n0 + (wave >> 1) * (BN / 2) + (KG == 2 ? grp * (BN / 4) : 0) + 8 * lane_n);
     const int t_wave = (wave & 1) * (BT / 2);
 #pragma unroll 1
     for (int p = 0; p < FT / PT; ++p) {
@@ -574,24 +596,37 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
                     }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        // the next token's sums and residuals are asked for before this one's are finished
-        int t = lane / LPT;
+        // U tokens at a time: one wavefront a SIMD hides no latency of another's.  Residuals are asked for
+        // one round ahead; without them nothing in the loop waits for memory.
         const int t_first = t_wave + p * 32;
-        half8 res = a.planes ? half8{} : cols.residual(a, t0 + t_first + t);
-        i32x4 lo = mine[t * CW + ((2 * lane_n) ^ (t & 7))], hi = mine[t * CW + ((2 * lane_n + 1) ^ (t & 7))];
+        auto tokens = [&](auto residuals) {
+            constexpr bool RES = decltype(residuals)::value != 0;
+            constexpr int U = 32 / TPI < 4 ? 32 / TPI : 4;
+            half8 next[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) next[u] = RES ? cols.residual(a, t0 + t_first + lane / LPT + u * TPI) : half8{};
 #pragma unroll 1
-        for (; t < 32; t += TPI) {
-            const int tn = min(t + TPI, 31);
-            const half8 res_next = a.planes ? half8{} : cols.residual(a, t0 + t_first + tn);
-            const i32x4 lo_next = mine[tn * CW + ((2 * lane_n) ^ (tn & 7))];
-            const i32x4 hi_next = mine[tn * CW + ((2 * lane_n + 1) ^ (tn & 7))];
-            const f32x4 lo_f = __builtin_bit_cast(f32x4, lo), hi_f = __builtin_bit_cast(f32x4, hi);
-            if (a.planes) cols.store_plane(a, blockIdx.y, t0 + t_first + t, lo_f, hi_f);
-            else cols.finish(a, t0 + t_first + t, lo_f, hi_f, E4M3 ? s_scale[t_first + t] : 1.0f, res);
-            res = res_next;
-            lo = lo_next;
-            hi = hi_next;
-        }
+            for (int tb = lane / LPT; tb < 32; tb += U * TPI) {
+                int t[U];
+                f32x4 lo[U], hi[U];
+                float sx[U];
+                half8 res[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int tt = tb + u * TPI;
+                    t[u] = t0 + t_first + tt;
+                    lo[u] = __builtin_bit_cast(f32x4, mine[tt * CW + ((2 * lane_n) ^ (tt & 7))]);
+                    hi[u] = __builtin_bit_cast(f32x4, mine[tt * CW + ((2 * lane_n + 1) ^ (tt & 7))]);
+                    sx[u] = E4M3 ? s_scale[t_first + tt] : 1.0f;
+                    res[u] = next[u];
+                    if constexpr (RES) next[u] = cols.residual(a, min(t[u] + U * TPI, a.T - 1));
+                }
+                cols.finish(a, t, lo, hi, sx, res);
+            }
+            if constexpr (RES) __builtin_amdgcn_s_waitcnt(kNoLoads);
+        };
+        if (a.res) tokens(Const<1>{});
+        else tokens(Const<0>{});
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
     }
