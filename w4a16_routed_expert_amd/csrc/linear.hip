@@ -324,13 +324,16 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 // banks (a load's 64 lanes fill 1024 consecutive bytes of LDS: the swizzle is
 // in the addresses they read from).
 //   Bound by the matrix cores for large products, whose clock then falls (8192^3
-// FP16 832 us = 1.32 PFLOP/s, e4m3 410 us = 2.68; 8192 x 5632 x 4096 e4m3 182 us =
-// 2.08, 195 with bias and SiLU, whose two transcendental instructions a value
-// nothing overlaps; FP16 324 us = 1.17), by LDS with 128 x 128 tiles (64 KB read and
+// FP16 832 us = 1.32 PFLOP/s, e4m3 403 us = 2.73; 8192 x 5632 x 4096 e4m3 163 us =
+// 2.32, 174 with bias and SiLU, whose two transcendental instructions a value
+// nothing overlaps; FP16 319 us = 1.18), by LDS with 128 x 128 tiles (64 KB read and
 // 32 KB written a step against 512 cycles of matrix instructions: 1333 x 2817 x
-// 2048 FP16 24 us).  Rows that do not start at multiples of 128 bytes cost a
-// second cache line a step (K 2064: 29 us); loading two steps of a row together so
-// that they share lines took 7 % off that and cost aligned rows 10 %.
+// 2064 FP16 27 us).  Of a 256 x 256 tile's 111 k cycles (e4m3, K 4096) the loop takes
+// 85 k (65 k of matrix instructions), the epilogue 19 k (28 k with SiLU); finishing
+// one token at a time, each wait for a residual one for the stores before it, it
+// took 42 k.  Rows that do not start at multiples of 128 bytes cost a second cache
+// line a step; loading two steps of a row together so that they share lines took
+// 7 % off that and cost aligned rows 10 %.
 template <int OUTSTANDING>
 __device__ inline void arrive()
 {
@@ -712,8 +715,8 @@ double rounds(long long tiles, int slots, double cost, double least)
 // steps of k in one round of loads, and 32 rows a block where that leaves a block a CU and k still is
 // one round (FP16 W of more than that streams at HBM's rate with 16 rows).  Then the 64 x 32 tiles (k
 // in four groups of wavefronts) while they fill no more than one round of the 256 CUs.  Then by the time
-// of the rounds, whose costs relative to 128 x 128 tiles with two blocks a CU are measured ones (FP16 72
-// us and e4m3 35 us a round at K 4096; a 256 x 256 tile's start and end weigh more when k is short).
+// of the rounds, whose costs relative to 128 x 128 tiles with two blocks a CU are measured ones (FP16 64
+// us and e4m3 34 us a round at K 4096; a 256 x 256 tile's start and end weigh more when k is short).
 // Measured (us, FP16 / e4m3; 128 x 128 with two groups of wavefronts (g) and two blocks a CU (b)):
 //   1 x 2048 x 1024: stream with 4 wavefronts 3.2 / 3.3, 8 3.8 / 3.7; K 2048: 5.6 / 3.6, 4.8 / 4.0
 //   16 x 5632 x 2048: 8 wavefronts, 16 rows 10.5 / 7.9, 32 rows 8.3 / 6.0; e4m3 4 wavefronts, 32 rows 5.4
@@ -723,17 +726,19 @@ double rounds(long long tiles, int slots, double cost, double least)
 //   4, 8, 16 x 65536 x 2048 FP16: stream 53.6, 60.1, 72.4, 64 x 32 tiles 61.4, 62.3, 63.5
 //   32 x 5632 x 2048: stream 13.2 / 9.3, 64 x 32 tiles 8.8 / 6.6
 //   256 x 2048 x 2048: 64 x 32 tiles 7.4 / 5.9, 64 x 64 9.1 / 6.5
-//   256 x 5632 x 2048: 64 x 32 tiles 21 / 15, 64 x 64 15 / 9.9, 128 x 128 (g) 19 / 13
-//   512 x 5632 x 4096: 64 x 64 45 / 25, 128 x 128 (g) 33 / 20, (b) 41 / 25, 256 x 256 79 / 55
-//   1333 x 2817 x 2064: 64 x 64 40 / 25, 128 x 128 (g) 29 / 18, (b) 33 / 20, 256 x 256 56 / 43
-//   2048 x 4096 x 4096: 128 x 128 (g) 79 / 43, (b) 74 / 38, 256 x 256 92 / 58
-//   2048 x 5632 x 4096: 128 x 128 (g) 112 / 61, (b) 117 / 59, 256 x 256 107 / 60
-//   4096 x 4096 x 4096: 128 x 128 (g) 159 / 83, (b) 144 / 75, 256 x 256 138 / 70
-//   4096 x 4096 x 1024: 128 x 128 (g) 51 / 36, (b) 43 / 31, 256 x 256 45 / 36
+//   256 x 5632 x 2048: 64 x 32 tiles 21 / 15, 64 x 64 14 / 9.9, 128 x 128 (g) 18 / 12
+//   512 x 5632 x 4096: 64 x 64 43 / 23, 128 x 128 (g) 32 / 19, (b) 39 / 23, 256 x 256 69 / 45
+//   1333 x 2817 x 2064: 64 x 64 39 / 23, 128 x 128 (g) 27 / 17, (b) 31 / 18, 256 x 256 46 / 33
+//   2048 x 4096 x 4096: 128 x 128 (g) 74 / 41, (b) 64 / 34, 256 x 256 82 / 51
+//   2048 x 5632 x 4096: 128 x 128 (g) 113 / 59, (b) 114 / 53, 256 x 256 92 / 52
+//   3000 x 5632 x 2048: 128 x 128 (g) 97 / 58, (b) 83 / 47, 256 x 256 100 / 62
+//   4096 x 4096 x 512: 128 x 128 (b) 26 / 20, 256 x 256 27 / 21
+//   4096 x 4096 x 4096: 128 x 128 (g) 160 / 82, (b) 136 / 66, 256 x 256 116 / 58
+//   500 x 65536 x 2048: 64 x 64 274 / 162, 128 x 128 (b) 167 / 100, 256 x 256 140 / 82
 //   70 x 65536 x 2048: 64 x 64 82 / 47, 128 x 128 (b) 74 / 34, 256 x 256 84 / 46
-// 128 x 128 tiles in FP16 with 32 x 32 instructions: (g) 30 and (b) 34 at 1333 x 2817 x 2064; 256 x 256
-// ones with 16 x 16 instructions 78 there and 152 at 4096 x 4096 x 4096, as their accumulators do not
-// stay in place.  With four stages instead of two groups a 128 x 128 tile took 33 / 19.
+// 128 x 128 tiles in FP16 with 32 x 32 instructions: (g) 5 %, (b) 2 to 8 % slower; 256 x 256 ones with
+// 16 x 16 instructions 10 % and more, as their accumulators do not stay in place.  With four stages
+// instead of two groups a 128 x 128 tile took 33 / 19 at 1333 x 2817 x 2064 (two groups then 29 / 18).
 template <bool E4M3>
 void launch(const LinearArgs &a, void *ws, hipStream_t s)
 {
@@ -754,7 +759,7 @@ void launch(const LinearArgs &a, void *ws, hipStream_t s)
     if (tiles(64, 32) <= 256) return launch_tile<E4M3, 64, 32, 16, 2, 4>(a, splits_of(a, tiles(64, 32)), ws, s);
     const double small = rounds(tiles(64, 64), 512, 0.45, 0.5), deep = rounds(tiles(128, 128), 256, 0.6, 0.5);
     const double two = rounds(tiles(128, 128), 512, 1.0, 0.5);
-    const double large = rounds(tiles(256, 256), 256, 1.64 * (steps + 14) / (steps + 7), 0.65);
+    const double large = rounds(tiles(256, 256), 256, 1.55 + 12.0 / (steps + 16), 0.65);
     const double best = std::min(std::min(small, deep), std::min(two, large));
     if (small == best) return launch_tile<E4M3, 64, 64, 16, 4>(a, 1, ws, s);
     if (deep == best) return launch_tile<E4M3, 128, 128, 16, 2, 2>(a, 1, ws, s);
