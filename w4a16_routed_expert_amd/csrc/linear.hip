@@ -505,6 +505,13 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     constexpr int CW = BN / 16 * NH, LPT = CW / 2;               // 4-output chunks of its row; lanes that finish a token
     Columns<E4M3> cols;
     if constexpr (KG != 4) cols.load(a, n0 + (wave >> 1) * (BN / 2) + (KG == 2 ? grp * (BN / 4) : 0) + lane % LPT * 8);
+    // tokens finished at once, and the first ones' residuals; the next ones' follow, a round ahead
+    constexpr int TPI = 64 / LPT, U = 32 / TPI < 4 ? 32 / TPI : 4;   // tokens a wavefront holds; rounds of them at once
+    const int t_wave = (wave & 1) * (BT / 2);
+    half8 next[U];
+    if constexpr (KG != 4)
+#pragma unroll
+        for (int u = 0; u < U; ++u) next[u] = cols.residual(a, t0 + t_wave + lane / LPT + u * TPI);
     // No load is on its way to LDS any more.  The builtin tells the compiler, which would else wait for
     // memory (and so for the stores before) at every use of LDS below.
     __builtin_amdgcn_s_waitcnt(kNoLoads);
@@ -579,9 +586,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     constexpr int PT = 32 / MT;                                  // token tiles at a time
     static_assert(32 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
     i32x4 *mine = ((wave & 2) ? (part<E4M3, BN, BT, MT, KG, 1, 0>() + grp * (BT * 8)) : (part<E4M3, BN, BT, MT, KG, 0, 0>() + grp * (BT * 8))) + (wave & 1) * (32 * CW);
-    constexpr int TPI = 64 / LPT;                                // tokens at once
     const int lane_n = lane % LPT;
-    const int t_wave = (wave & 1) * (BT / 2);
 #pragma unroll 1
     for (int p = 0; p < FT / PT; ++p) {
 #pragma unroll
@@ -599,15 +604,11 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
                     }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        // U tokens at a time: one wavefront a SIMD hides no latency of another's.  Residuals are asked for
-        // one round ahead; without them nothing in the loop waits for memory.
+        // U tokens a lane at a time: one wavefront a SIMD hides no latency of another's.  Without residuals
+        // nothing in the loop waits for memory (a wait for a load is one for the stores before it).
         const int t_first = t_wave + p * 32;
         auto tokens = [&](auto residuals) {
             constexpr bool RES = decltype(residuals)::value != 0;
-            constexpr int U = 32 / TPI < 4 ? 32 / TPI : 4;
-            half8 next[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) next[u] = RES ? cols.residual(a, t0 + t_first + lane / LPT + u * TPI) : half8{};
 #pragma unroll 1
             for (int tb = lane / LPT; tb < 32; tb += U * TPI) {
                 int t[U];
@@ -621,12 +622,13 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
                     lo[u] = __builtin_bit_cast(f32x4, mine[tt * CW + ((2 * lane_n) ^ (tt & 7))]);
                     hi[u] = __builtin_bit_cast(f32x4, mine[tt * CW + ((2 * lane_n + 1) ^ (tt & 7))]);
                     sx[u] = E4M3 ? s_scale[t_first + tt] : 1.0f;
-                    res[u] = next[u];
-                    if constexpr (RES) next[u] = cols.residual(a, min(t[u] + U * TPI, a.T - 1));
+                    res[u] = RES ? next[u] : half8{};
                 }
+                if constexpr (RES)
+#pragma unroll
+                    for (int u = 0; u < U; ++u) next[u] = cols.residual(a, t[u] + U * TPI);
                 cols.finish(a, t, lo, hi, sx, res);
             }
-            if constexpr (RES) __builtin_amdgcn_s_waitcnt(kNoLoads);
         };
         if (a.res) tokens(Const<1>{});
         else tokens(Const<0>{});
