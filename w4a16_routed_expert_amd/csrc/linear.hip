@@ -433,6 +433,19 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[h][j][i] = (typename S::Acc)(0.0f);
 
+    // four groups: a lane finishes 8 outputs of one token at the end, whose operands arrive meanwhile
+    constexpr int ITEMS = BT * BN / 8;
+    static_assert(KG != 4 || ITEMS <= 256 * KG, "one item a thread");
+    const int it = threadIdx.x / (BN / 8), ic = threadIdx.x % (BN / 8) * 2;    // its token; its 4-output chunk
+    Columns<E4M3> cols;
+    half8 own = {};
+    if constexpr (KG == 4) {
+        if ((int)threadIdx.x < ITEMS) {
+            cols.load(a, n0 + 4 * ic);
+            if (!a.planes) own = cols.residual(a, t0 + it);
+        }
+    }
+
     typename S::Operand x[P][FT], wa[P][HN], wb[P][HN];
     constexpr int XA = LX + LW;
     fetch_xa(Const<0>{}, 0, XA, 0);
@@ -503,7 +516,6 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     }
     constexpr int NH = KG == 2 ? 1 : 2;                          // halves of its output rows a wavefront finishes
     constexpr int CW = BN / 16 * NH, LPT = CW / 2;               // 4-output chunks of its row; lanes that finish a token
-    Columns<E4M3> cols;
     if constexpr (KG != 4) cols.load(a, n0 + (wave >> 1) * (BN / 2) + (KG == 2 ? grp * (BN / 4) : 0) + lane % LPT * 8);
     // tokens finished at once, and the first ones' residuals; the next ones' follow, a round ahead
     constexpr int TPI = 64 / LPT, U = 32 / TPI < 4 ? 32 / TPI : 4;   // tokens a wavefront holds; rounds of them at once
@@ -520,7 +532,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     if constexpr (KG == 4) {
         // the groups' sums meet in LDS, [group][token][output], two groups a
         // stage of X; then a lane finishes 8 outputs of a token
-        constexpr int ROW = BN / 4, ITEMS = BT * BN / 8;         // 4-output chunks of a token; lanes of work
+        constexpr int ROW = BN / 4;                              // 4-output chunks of a token
         static_assert(MT == 16 && 2 * BT * ROW <= KG * BT * 8, "two groups' sums fit a stage");
         i32x4 *const x0 = part<E4M3, BN, BT, MT, KG, 0, 0>(), *const x1 = part<E4M3, BN, BT, MT, KG, 1, 0>();
         i32x4 *mine = (grp & 2 ? x1 : x0) + (grp & 1) * (BT * ROW);
@@ -532,20 +544,16 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
                 mine[t * ROW + (c ^ (t & 7))] = __builtin_bit_cast(i32x4, acc[i / HN][j][i % HN]);
             }
         __syncthreads();
-        for (int o = threadIdx.x; o < ITEMS; o += 256 * KG) {
-            const int t = o / (BN / 8), c = o % (BN / 8) * 2;
-            Columns<E4M3> cols;
-            cols.load(a, n0 + 4 * c);
-            const half8 res = a.planes ? half8{} : cols.residual(a, t0 + t);
+        if ((int)threadIdx.x < ITEMS) {
             f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
 #pragma unroll
             for (int q = 0; q < KG; ++q) {
-                const i32x4 *p = (q & 2 ? x1 : x0) + (q & 1) * (BT * ROW) + t * ROW;
-                lo += __builtin_bit_cast(f32x4, p[c ^ (t & 7)]);
-                hi += __builtin_bit_cast(f32x4, p[(c + 1) ^ (t & 7)]);
+                const i32x4 *p = (q & 2 ? x1 : x0) + (q & 1) * (BT * ROW) + it * ROW;
+                lo += __builtin_bit_cast(f32x4, p[ic ^ (it & 7)]);
+                hi += __builtin_bit_cast(f32x4, p[(ic + 1) ^ (it & 7)]);
             }
-            if (a.planes) cols.store_plane(a, blockIdx.y, t0 + t, lo, hi);
-            else cols.finish(a, t0 + t, lo, hi, E4M3 ? s_scale[t] : 1.0f, res);
+            if (a.planes) cols.store_plane(a, blockIdx.y, t0 + it, lo, hi);
+            else cols.finish(a, t0 + it, lo, hi, E4M3 ? s_scale[it] : 1.0f, own);
         }
         return;
     } else {
