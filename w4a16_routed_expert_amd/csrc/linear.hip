@@ -724,9 +724,10 @@ double rounds(long long tiles, int slots, double cost, double least)
 // bytes as of W at 16 tokens, are in the way (FP16, many outputs); with as many wavefronts as take the
 // steps of k in one round of loads, and 32 rows a block where that leaves a block a CU and k still is
 // one round (FP16 W of more than that streams at HBM's rate with 16 rows).  Then the 64 x 32 tiles (k
-// in four groups of wavefronts) while they fill no more than one round of the 256 CUs.  Then by the time
-// of the rounds, whose costs relative to 128 x 128 tiles with two blocks a CU are measured ones (FP16 64
-// us and e4m3 34 us a round at K 4096; a 256 x 256 tile's start and end weigh more when k is short).
+// in four groups of wavefronts; two stages of LDS for up to four steps a group, else three) while they
+// fill no more than one round of the 256 CUs.  Then by the time of the rounds, whose costs relative to
+// 128 x 128 tiles with two blocks a CU are measured ones (FP16 64 us and e4m3 34 us a round at K 4096; a
+// 256 x 256 tile's start and end weigh more when k is short).
 // Measured (us, FP16 / e4m3; 128 x 128 with two groups of wavefronts (g) and two blocks a CU (b)):
 //   1 x 2048 x 1024: stream with 4 wavefronts 3.2 / 3.3, 8 3.8 / 3.7; K 2048: 5.6 / 3.6, 4.8 / 4.0
 //   16 x 5632 x 2048: 8 wavefronts, 16 rows 10.5 / 7.9, 32 rows 8.3 / 6.0; e4m3 4 wavefronts, 32 rows 5.4
@@ -734,8 +735,9 @@ double rounds(long long tiles, int slots, double cost, double least)
 //   16 x 2048 x 2048: stream 6.1 / 4.3, 64 x 32 tiles 8.1 / 5.5
 //   4, 8, 16 x 16384 x 4096 FP16: stream 28.6, 31.7, 38.2, 64 x 32 tiles 29.2, 29.3, 29.6
 //   4, 8, 16 x 65536 x 2048 FP16: stream 53.6, 60.1, 72.4, 64 x 32 tiles 61.4, 62.3, 63.5
-//   32 x 5632 x 2048: stream 13.2 / 9.3, 64 x 32 tiles 8.8 / 6.6
-//   256 x 2048 x 2048: 64 x 32 tiles 7.4 / 5.9, 64 x 64 9.1 / 6.5
+//   32 x 5632 x 2048: stream 13.2 / 9.3, 64 x 32 tiles with two stages 8.9 / 6.3, three 8.2 / 6.4
+//   17 x 2048 x 1024 e4m3: 64 x 32 tiles with two stages 4.4, three 4.5
+//   256 x 2048 x 2048: 64 x 32 tiles 8.1 / 6.0, 64 x 64 9.1 / 6.5
 //   256 x 5632 x 2048: 64 x 32 tiles 21 / 15, 64 x 64 14 / 9.9, 128 x 128 (g) 18 / 12
 //   512 x 5632 x 4096: 64 x 64 43 / 23, 128 x 128 (g) 32 / 19, (b) 39 / 23, 256 x 256 69 / 45
 //   1333 x 2817 x 2064: 64 x 64 39 / 23, 128 x 128 (g) 27 / 17, (b) 31 / 18, 256 x 256 46 / 33
@@ -766,7 +768,11 @@ void launch(const LinearArgs &a, void *ws, hipStream_t s)
         else stream(Const<8>{}, Const<1>{});
         return;
     }
-    if (tiles(64, 32) <= 256) return launch_tile<E4M3, 64, 32, 16, 2, 4>(a, splits_of(a, tiles(64, 32)), ws, s);
+    if (tiles(64, 32) <= 256) {
+        const int splits = splits_of(a, tiles(64, 32));
+        if (steps <= 16) return launch_tile<E4M3, 64, 32, 16, 2, 4>(a, splits, ws, s);
+        return launch_tile<E4M3, 64, 32, 16, 3, 4>(a, splits, ws, s);
+    }
     const double small = rounds(tiles(64, 64), 512, 0.45, 0.5), deep = rounds(tiles(128, 128), 256, 0.6, 0.5);
     const double two = rounds(tiles(128, 128), 512, 1.0, 0.5);
     const double large = rounds(tiles(256, 256), 256, 1.55 + 12.0 / (steps + 16), 0.65);
