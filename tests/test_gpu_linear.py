@@ -250,3 +250,11 @@ def test_many_tokens_and_outputs_with_a_long_sum(type):
     c.check_whole(c.run(), "3990x3993x4112")
     c = Case(3990, 3985, 4112, type, whole=False)
     c.check(c.run(SILU), SILU, "3990x3985x4112 silu")
+
+
+@pytest.mark.parametrize("type", [FP16, E4M3], ids=["fp16", "e4m3"])
+@pytest.mark.parametrize("T,N,K", [(1, 17, 1 << 20), (16, 33, 1 << 20), (40, 70, 1 << 20), (65536, 5, 16), (65536, 67, 48),
+                                   (1, 1 << 20, 16), (18, 1 << 18, 32)])
+def test_the_largest_sizes(T, N, K, type):
+    c = Case(T, N, K, type, whole=True)
+    c.check_whole(c.run(), f"{T}x{N}x{K}")

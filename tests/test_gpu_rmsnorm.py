@@ -198,3 +198,8 @@ def test_captured_and_on_another_stream():
         torch.cuda.synchronize()
         got = {n: t.cpu().numpy() for n, t in (*out.items(), ("q", q), ("q_scale", scale))}
         same(got, expected(x2, y2, w), f"replay {step}")
+
+
+@pytest.mark.parametrize("T,H", [(256, 1024), (257, 1024), (300, 513), (1001, 777), (260, 1000), (5000, 512), (3000, 2048)])
+def test_longer_batches(T, H):
+    test_equals_the_definition(T, H)

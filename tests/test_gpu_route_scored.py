@@ -290,3 +290,14 @@ def test_logits_are_correctly_rounded_at_every_magnitude(T, xs, ws):
     call(*device(x, w), None, score=SIGMOID)
     want = oracle.router_logits(x, w)
     check(call.host(), expected(want, 4, None, score=SIGMOID), want, f"T={T}")
+
+
+@pytest.mark.parametrize("T,H,E,k", [(65536, 128, 64, 8), (65536, 128, 3, 1), (300, 4096, 64, 8), (64, 4096, 64, 8)])
+def test_the_largest_batches_and_rows(T, H, E, k):
+    x, wr, bias = inputs(T, H, E, 5)
+    call = Call(T, H, E, k)
+    logits = oracle.router_logits(x, wr)
+    xd, wd, bd = device(x, wr, bias)
+    for _ in range(2):
+        call(xd, wd, bd, score=SIGMOID)
+        check(call.host(), expected(logits, k, bias, score=SIGMOID), logits, f"T={T} E={E}")
