@@ -242,17 +242,18 @@ def _current_stream() -> int:
 
 
 def _begin(t, stream):
-    """(device ordinal of a call's first argument, handle of its stream): ordinal -1 for an address or
-    nothing, which is taken as the current device's; no handle if the device is not the current one."""
+    """(device ordinal of a call's first argument, handle of its stream, the argument's address): ordinal
+    -1 for an address or nothing, which is taken as the current device's; no handle if the device is not
+    the current one."""
     if t is None or isinstance(t, int):
-        return -1, _s(stream)
+        return -1, _s(stream), t
     d = t.get_device()
     if d < 0:
         raise ValueError("a tensor is not in GPU memory")
     c = _torch_c or _c()
     if d != c._cuda_getDevice():
-        return d, None
-    return d, c._cuda_getCurrentRawStream(d) if stream is None else _s(stream)
+        return d, None, None
+    return d, c._cuda_getCurrentRawStream(d) if stream is None else _s(stream), t.data_ptr()
 
 
 def _g(t, dev: int):
@@ -268,7 +269,7 @@ def _g(t, dev: int):
 def _there(d: int, call, args: dict):
     """`call` with device d current, so that its stream and launches are that device's."""
     import torch
-    del args["d"], args["s"]
+    del args["d"], args["s"], args["p"]
     with torch.cuda.device(d):
         return call(**args)
 
@@ -336,13 +337,15 @@ def route_rule(score=MOE_SCORE_SOFTMAX, n_group=1, topk_group=1, group_score=MOE
 
 def moe_route_scored(x, w_router, select_bias, T, H, E, k, rule: RouteRule, logits, topk_ids, topk_w, expert_offsets,
                      sorted_pairs, pair_pos, active_list, n_active, ws, ws_bytes, stream=None):
-    d, s = _begin(x, stream)
+    d, s, p = _begin(x, stream)
     if s is None:
         return _there(d, moe_route_scored, locals())
-    _check(load().moe_route_scored(_g(x, d), _g(w_router, d), _g(select_bias, d), T, H, E, k,
-                                   None if rule is None else ctypes.byref(rule), _g(logits, d), _g(topk_ids, d),
-                                   _g(topk_w, d), _g(expert_offsets, d), _g(sorted_pairs, d), _g(pair_pos, d),
-                                   _g(active_list, d), _g(n_active, d), _g(ws, d), ws_bytes, s))
+    rc = (_lib or load()).moe_route_scored(p, _g(w_router, d), _g(select_bias, d), T, H, E, k,
+                                           None if rule is None else ctypes.byref(rule), _g(logits, d), _g(topk_ids, d),
+                                           _g(topk_w, d), _g(expert_offsets, d), _g(sorted_pairs, d), _g(pair_pos, d),
+                                           _g(active_list, d), _g(n_active, d), _g(ws, d), ws_bytes, s)
+    if rc:
+        _check(rc)
 
 
 def moe_w4a16_gateup(x, T, H, I, E, k, rows, row_stride, slot_map, expert_offsets, sorted_pairs, active_list,
@@ -459,12 +462,14 @@ def _ld(t, ld, width):
 def moe_residual_rmsnorm(x, y, w, eps, T, H, sum_out=None, norm=None, q=None, q_scale=None, ldx=None, ldy=None,
                          ld_sum=None, ld_norm=None, ldq=None, stream=None):
     """Row strides (elements) are those of 2-D tensors unless given."""
-    d, s = _begin(x, stream)
+    d, s, p = _begin(x, stream)
     if s is None:
         return _there(d, moe_residual_rmsnorm, locals())
-    _check(load().moe_residual_rmsnorm(_g(x, d), _ld(x, ldx, H), _g(y, d), _ld(y, ldy, H), _g(w, d), eps, T, H,
-                                       _g(sum_out, d), _ld(sum_out, ld_sum, H), _g(norm, d), _ld(norm, ld_norm, H),
-                                       _g(q, d), _ld(q, ldq, H), _g(q_scale, d), s))
+    rc = (_lib or load()).moe_residual_rmsnorm(p, _ld(x, ldx, H), _g(y, d), _ld(y, ldy, H), _g(w, d), eps, T, H,
+                                               _g(sum_out, d), _ld(sum_out, ld_sum, H), _g(norm, d),
+                                               _ld(norm, ld_norm, H), _g(q, d), _ld(q, ldq, H), _g(q_scale, d), s)
+    if rc:
+        _check(rc)
 
 
 def moe_linear_workspace_size(T: int, N: int, K: int, type: int) -> int:
@@ -474,12 +479,14 @@ def moe_linear_workspace_size(T: int, N: int, K: int, type: int) -> int:
 def moe_linear(x, w, T, N, K, type, y, x_scale=None, w_scale=None, bias=None, act=MOE_ACT_NONE, residual=None,
                ws=None, ws_bytes=0, ldx=None, ldw=None, ldr=None, ldy=None, stream=None):
     """Row strides (elements) are those of 2-D tensors unless given."""
-    d, s = _begin(x, stream)
+    d, s, p = _begin(x, stream)
     if s is None:
         return _there(d, moe_linear, locals())
-    _check(load().moe_linear(_g(x, d), _ld(x, ldx, K), _g(x_scale, d), _g(w, d), _ld(w, ldw, K), _g(w_scale, d),
-                             _g(bias, d), _g(residual, d), _ld(residual, ldr, N), T, N, K, type, act, _g(y, d),
-                             _ld(y, ldy, N), _g(ws, d), ws_bytes, s))
+    rc = (_lib or load()).moe_linear(p, _ld(x, ldx, K), _g(x_scale, d), _g(w, d), _ld(w, ldw, K), _g(w_scale, d),
+                                     _g(bias, d), _g(residual, d), _ld(residual, ldr, N), T, N, K, type, act, _g(y, d),
+                                     _ld(y, ldy, N), _g(ws, d), ws_bytes, s)
+    if rc:
+        _check(rc)
 
 
 # ------------------------------------------------------------------ resident expert table
