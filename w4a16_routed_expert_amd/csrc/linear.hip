@@ -390,41 +390,47 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     const int chunks = min(a.chunks - 8 * step0, 8 * a.split_steps), steps = (chunks + 8 * KG - 1) / (8 * KG);
     const __amdgpu_buffer_rsrc_t rw = rows_rsrc(a.w + n0 * a.ldw + 128 * step0, a.ldw, min(BN, a.N - n0), chunks);
     const __amdgpu_buffer_rsrc_t rx = rows_rsrc(a.x + t0 * a.ldx + 128 * step0, a.ldx, min(BT, a.T - t0), chunks);
-    const int lr = lane >> 3, lc = (lane & 7) ^ ((lr >> 1) + 4 * (wave & 1));   // row within a load, chunk of it
+    // Two groups: a row of LDS holds both groups' steps, 16 chunks that all wavefronts load together (256
+    // consecutive bytes of a row touch fewer cache lines than twice 128 where they straddle them).
+    constexpr bool WIDE = KG == 2;
+    static_assert(!WIDE || MT == 16, "the swizzle of 16 chunks is of 16 rows");
+    constexpr int RC = WIDE ? 16 : 8, NW = WIDE ? 8 : 4, LR = 64 / RC;          // chunks of a row; wavefronts; rows of a load
+    const int lw = WIDE ? all_waves : wave, lr = lane / RC;                     // row within a load
+    const int lc = (lane % RC) ^ (WIDE ? 4 * (all_waves & 3) + lr : (lr >> 1) + 4 * (wave & 1));   // chunk of it
     uint32_t off_x[LX], off_a[LW], off_b[LW];
 #pragma unroll
     for (int i = 0; i < LX; ++i) {
-        const int row = 8 * (i * 4 + wave) + lr;
+        const int row = LR * (i * NW + lw) + lr;
         off_x[i] = t0 + row < a.T ? (uint32_t)(row * a.ldx) + 16u * lc : kOutside;
     }
 #pragma unroll
     for (int i = 0; i < LW; ++i) {
-        const int h = 8 * (i * 4 + wave) + lr, row = h / (BN / 4) * (BN / 2) + h % (BN / 4);
+        const int h = LR * (i * NW + lw) + lr, row = h / (BN / 4) * (BN / 2) + h % (BN / 4);
         off_a[i] = n0 + row < a.N ? (uint32_t)(row * a.ldw) + 16u * lc : kOutside;
         off_b[i] = n0 + row + BN / 4 < a.N ? (uint32_t)((row + BN / 4) * a.ldw) + 16u * lc : kOutside;
     }
     // load i of a part of step `step` (zeros past the last chunk)
     auto fetch = [&](uint32_t off, const __amdgpu_buffer_rsrc_t &rsrc, i32x4 *s, int i, int step) {
         // uniform, but not always seen to be: a divergent scalar offset would become a loop over lanes
-        const int at = __builtin_amdgcn_readfirstlane(step * KG + grp);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(s + (i * 4 + wave) * 64), 16,
-                                                 8 * at + lc < chunks ? off : kOutside, 128 * at, 0, 0);
+        const int at = __builtin_amdgcn_readfirstlane(WIDE ? step : step * KG + grp);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(s + (i * NW + lw) * 64), 16,
+                                                 RC * at + lc < chunks ? off : kOutside, 16 * RC * at, 0, 0);
     };
     // loads [i0, i1) of X, then WA; of WB
     auto fetch_xa = [&](auto st, int i0, int i1, int step) {
 #pragma unroll
         for (int i = i0; i < i1; ++i) {
-            if (i < LX) fetch(off_x[i], rx, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 0>() + grp * (BT * 8)), i, step);
-            else fetch(off_a[i - LX], rw, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 1>() + grp * (BN * 4)), i - LX, step);
+            if (i < LX) fetch(off_x[i], rx, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 0>() + (WIDE ? 0 : grp) * (BT * 8)), i, step);
+            else fetch(off_a[i - LX], rw, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 1>() + (WIDE ? 0 : grp) * (BN * 4)), i - LX, step);
         }
     };
     auto fetch_b = [&](auto st, int i0, int i1, int step) {
 #pragma unroll
-        for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 2>() + grp * (BN * 4)), i, step);
+        for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 2>() + (WIDE ? 0 : grp) * (BN * 4)), i, step);
     };
-    const int swz = (r >> 1) & 7;
-    const int at_x = ((wave & 1) * (BT / 2) + r) * 8, at_w = ((wave >> 1) * (BN / 4) + r) * 8;
-    auto read = [&](const i32x4 *s, int at, int part) { return S::read(s + at, g, swz, part); };
+    const int swz = WIDE ? r : (r >> 1) & 7, rg = WIDE ? 8 * grp + g : g;
+    const int at_x = ((wave & 1) * (BT / 2) + r) * RC, at_w = ((wave >> 1) * (BN / 4) + r) * RC;
+    auto read = [&](const i32x4 *s, int at, int part) { return S::read(s + at, rg, swz, part); };
     typename S::Acc acc[2][FT][HN];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -463,9 +469,9 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
     for (int h = 0; h < P; ++h) {
 #pragma unroll
-        for (int j = 0; j < FT; ++j) x[h][j] = read((part<E4M3, BN, BT, MT, KG, 0, 0>() + grp * (BT * 8)), at_x + j * (MT * 8), h);
+        for (int j = 0; j < FT; ++j) x[h][j] = read((part<E4M3, BN, BT, MT, KG, 0, 0>() + (WIDE ? 0 : grp) * (BT * 8)), at_x + j * (MT * RC), h);
 #pragma unroll
-        for (int i = 0; i < HN; ++i) wa[h][i] = read((part<E4M3, BN, BT, MT, KG, 0, 1>() + grp * (BN * 4)), at_w + i * (MT * 8), h);
+        for (int i = 0; i < HN; ++i) wa[h][i] = read((part<E4M3, BN, BT, MT, KG, 0, 1>() + (WIDE ? 0 : grp) * (BN * 4)), at_w + i * (MT * RC), h);
     }
     // Step k, its parts in stage st.  The scheduling barriers keep each token
     // tile's few loads and reads among its matrix instructions.
@@ -476,7 +482,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
-            if (q < P * HN) wb[q / HN][q % HN] = read((part<E4M3, BN, BT, MT, KG, ST, 2>() + grp * (BN * 4)), at_w + q % HN * (MT * 8), q / HN);
+            if (q < P * HN) wb[q / HN][q % HN] = read((part<E4M3, BN, BT, MT, KG, ST, 2>() + (WIDE ? 0 : grp) * (BN * 4)), at_w + q % HN * (MT * RC), q / HN);
             fetch_b(Const<LAST>{}, q * LW / (P * FT), (q + 1) * LW / (P * FT), k + B - 1);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[0][j][i] = S::mma(wa[h][i], x[h][j], acc[0][j][i]);
@@ -487,11 +493,11 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
-            if (q < P * HN) wa[q / HN][q % HN] = read((part<E4M3, BN, BT, MT, KG, NEXT, 1>() + grp * (BN * 4)), at_w + q % HN * (MT * 8), q / HN);
+            if (q < P * HN) wa[q / HN][q % HN] = read((part<E4M3, BN, BT, MT, KG, NEXT, 1>() + (WIDE ? 0 : grp) * (BN * 4)), at_w + q % HN * (MT * RC), q / HN);
             fetch_xa(st, q * XA / (P * FT), (q + 1) * XA / (P * FT), k + B);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[1][j][i] = S::mma(wb[h][i], x[h][j], acc[1][j][i]);
-            x[h][j] = read((part<E4M3, BN, BT, MT, KG, NEXT, 0>() + grp * (BT * 8)), at_x + j * (MT * 8), h);
+            x[h][j] = read((part<E4M3, BN, BT, MT, KG, NEXT, 0>() + (WIDE ? 0 : grp) * (BT * 8)), at_x + j * (MT * RC), h);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
