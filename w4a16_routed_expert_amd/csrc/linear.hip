@@ -324,16 +324,17 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 // banks (a load's 64 lanes fill 1024 consecutive bytes of LDS: the swizzle is
 // in the addresses they read from).
 //   Bound by the matrix cores for large products, whose clock then falls (8192^3
-// FP16 832 us = 1.32 PFLOP/s, e4m3 403 us = 2.73; 8192 x 5632 x 4096 e4m3 163 us =
-// 2.32, 174 with bias and SiLU, whose two transcendental instructions a value
-// nothing overlaps; FP16 319 us = 1.18), by LDS with 128 x 128 tiles (64 KB read and
+// FP16 821 us = 1.34 PFLOP/s, e4m3 386 us = 2.85; 8192 x 5632 x 4096 e4m3 163 us =
+// 2.32, 172 with bias and SiLU, whose two transcendental instructions a value
+// nothing overlaps; FP16 312 us = 1.21), by LDS with 128 x 128 tiles (64 KB read and
 // 32 KB written a step against 512 cycles of matrix instructions: 1333 x 2817 x
-// 2064 FP16 27 us).  Of a 256 x 256 tile's 111 k cycles (e4m3, K 4096) the loop takes
+// 2048 FP16 22 us).  Of a 256 x 256 tile's 111 k cycles (e4m3, K 4096) the loop takes
 // 85 k (65 k of matrix instructions), the epilogue 19 k (28 k with SiLU); finishing
 // one token at a time, each wait for a residual one for the stores before it, it
 // took 42 k.  Rows that do not start at multiples of 128 bytes cost a second cache
-// line a step; loading two steps of a row together so that they share lines took
-// 7 % off that and cost aligned rows 10 %.
+// line a step (K 2064 26 to 28 us); two groups load both their steps of a row
+// together so that they share lines (5 % off that), while one group that loads two
+// steps ahead together has a step less for them to arrive (aligned rows 10 % slower).
 template <int OUTSTANDING>
 __device__ inline void arrive()
 {
