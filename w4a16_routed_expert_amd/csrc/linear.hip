@@ -185,7 +185,10 @@ struct Step<true, 16> {
     typedef i32x8 Operand;
     typedef f32x4 Acc;
     static __device__ inline Operand pick(const i32x4 (&c)[2], int) { return join(c[0], c[1]); }
-    static __device__ inline Operand read(const i32x4 *row, int g, int swz, int) { return join(row[g ^ swz], row[(g + 4) ^ swz]); }
+    static __device__ inline Operand read(const i32x4 *row, int g, int swz, int)
+    {
+        return join(row[g ^ swz], row[(g + 4) ^ swz]);
+    }
     static __device__ inline Acc mma(Operand w, Operand x, Acc c)
     {
         return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, 0, 0, 0);
@@ -273,7 +276,8 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
                 const int c = 8 * (s + u * NW) + 4 * h + g;
 #pragma unroll
                 for (int i = 0; i < R; ++i)
-                    w[i][u][h] = __builtin_amdgcn_raw_buffer_load_b128(rw, c < a.chunks ? row_w[i] + 16u * c : kOutside, 0, 0);
+                    w[i][u][h] =
+                        __builtin_amdgcn_raw_buffer_load_b128(rw, c < a.chunks ? row_w[i] + 16u * c : kOutside, 0, 0);
             }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -316,11 +320,12 @@ __global__ __launch_bounds__(NW * 64) void linear_stream_kernel(LinearArgs a)
 //     barrier; ask for X, WA of step k + B; read X, WA of step k + 1; multiply WB(k) . X(k)
 // A part is overwritten after the barrier that follows the products it was
 // read for: every wavefront's reads of it have then returned, so the barriers
-// wait for loads from memory only.  Each load has B - 1 steps to arrive, and the reads of LDS
-// run under the matrix instructions: those of the next step's token tile j
-// replace tile j once it has met every row of WB.
+// wait for loads from memory only.  Each load has B - 1 steps to arrive, and the
+// reads of LDS run under the matrix instructions: those of the next step's token
+// tile j replace tile j once it has met every row of WB.
 //   A row of a step is 8 chunks of 16 bytes; chunk c of row r sits in slot
-// c ^ (r / 2 & 7), so the lanes that read one chunk of many rows spread over all
+// c ^ (r / 2 & 7) (two groups: 16 chunks, those of both groups' steps, in slot
+// c ^ (r & 15)), so the lanes that read one chunk of many rows spread over all
 // banks (a load's 64 lanes fill 1024 consecutive bytes of LDS: the swizzle is
 // in the addresses they read from).
 //   Bound by the matrix cores for large products, whose clock then falls (8192^3
@@ -364,7 +369,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     typedef Step<E4M3, MT> S;
     constexpr int P = S::kParts;
     constexpr int FT = BT / 2 / MT, HN = BN / 4 / MT;            // MT x MT tiles of a wavefront: along t; along half its n
-    constexpr int LX = BT / 32, LW = BN / 64;                    // loads (8 rows) of X and of a half of W a wavefront
+    constexpr int LX = BT / 32, LW = BN / 64;                    // loads (1 KB) of X and of a half of W a wavefront
     __shared__ float s_scale[E4M3 ? BT : 1];
     const int lane = threadIdx.x & 63, all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wave = all_waves & 3, grp = KG > 1 ? all_waves >> 2 : 0;
@@ -395,7 +400,8 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     // consecutive bytes of a row touch fewer cache lines than twice 128 where they straddle them).
     constexpr bool WIDE = KG == 2;
     static_assert(!WIDE || MT == 16, "the swizzle of 16 chunks is of 16 rows");
-    constexpr int RC = WIDE ? 16 : 8, NW = WIDE ? 8 : 4, LR = 64 / RC;          // chunks of a row; wavefronts; rows of a load
+    constexpr int RC = WIDE ? 16 : 8, LR = 64 / RC;                             // chunks of a row; rows of a load
+    constexpr int NW = WIDE ? 8 : 4;                                            // wavefronts that load a part
     const int lw = WIDE ? all_waves : wave, lr = lane / RC;                     // row within a load
     const int lc = (lane % RC) ^ (WIDE ? 4 * (all_waves & 3) + lr : (lr >> 1) + 4 * (wave & 1));   // chunk of it
     uint32_t off_x[LX], off_a[LW], off_b[LW];
@@ -417,17 +423,24 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(s + (i * NW + lw) * 64), 16,
                                                  RC * at + lc < chunks ? off : kOutside, 16 * RC * at, 0, 0);
     };
+    // a stage's X; its WA (1) or WB (2)
+    auto stage_x = [&](auto st) {
+        return part<E4M3, BN, BT, MT, KG, decltype(st)::value, 0>() + (WIDE ? 0 : grp) * (BT * 8);
+    };
+    auto stage_w = [&](auto st, auto ab) {
+        return part<E4M3, BN, BT, MT, KG, decltype(st)::value, decltype(ab)::value>() + (WIDE ? 0 : grp) * (BN * 4);
+    };
     // loads [i0, i1) of X, then WA; of WB
     auto fetch_xa = [&](auto st, int i0, int i1, int step) {
 #pragma unroll
         for (int i = i0; i < i1; ++i) {
-            if (i < LX) fetch(off_x[i], rx, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 0>() + (WIDE ? 0 : grp) * (BT * 8)), i, step);
-            else fetch(off_a[i - LX], rw, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 1>() + (WIDE ? 0 : grp) * (BN * 4)), i - LX, step);
+            if (i < LX) fetch(off_x[i], rx, stage_x(st), i, step);
+            else fetch(off_a[i - LX], rw, stage_w(st, Const<1>{}), i - LX, step);
         }
     };
     auto fetch_b = [&](auto st, int i0, int i1, int step) {
 #pragma unroll
-        for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, (part<E4M3, BN, BT, MT, KG, decltype(st)::value, 2>() + (WIDE ? 0 : grp) * (BN * 4)), i, step);
+        for (int i = i0; i < i1; ++i) fetch(off_b[i], rw, stage_w(st, Const<2>{}), i, step);
     };
     const int swz = WIDE ? r : (r >> 1) & 7, rg = WIDE ? 8 * grp + g : g;
     const int at_x = ((wave & 1) * (BT / 2) + r) * RC, at_w = ((wave >> 1) * (BN / 4) + r) * RC;
@@ -470,9 +483,9 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
     for (int h = 0; h < P; ++h) {
 #pragma unroll
-        for (int j = 0; j < FT; ++j) x[h][j] = read((part<E4M3, BN, BT, MT, KG, 0, 0>() + (WIDE ? 0 : grp) * (BT * 8)), at_x + j * (MT * RC), h);
+        for (int j = 0; j < FT; ++j) x[h][j] = read(stage_x(Const<0>{}), at_x + j * (MT * RC), h);
 #pragma unroll
-        for (int i = 0; i < HN; ++i) wa[h][i] = read((part<E4M3, BN, BT, MT, KG, 0, 1>() + (WIDE ? 0 : grp) * (BN * 4)), at_w + i * (MT * RC), h);
+        for (int i = 0; i < HN; ++i) wa[h][i] = read(stage_w(Const<0>{}, Const<1>{}), at_w + i * (MT * RC), h);
     }
     // Step k, its parts in stage st.  The scheduling barriers keep each token
     // tile's few loads and reads among its matrix instructions.
@@ -483,7 +496,7 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
-            if (q < P * HN) wb[q / HN][q % HN] = read((part<E4M3, BN, BT, MT, KG, ST, 2>() + (WIDE ? 0 : grp) * (BN * 4)), at_w + q % HN * (MT * RC), q / HN);
+            if (q < P * HN) wb[q / HN][q % HN] = read(stage_w(Const<ST>{}, Const<2>{}), at_w + q % HN * (MT * RC), q / HN);
             fetch_b(Const<LAST>{}, q * LW / (P * FT), (q + 1) * LW / (P * FT), k + B - 1);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[0][j][i] = S::mma(wa[h][i], x[h][j], acc[0][j][i]);
@@ -494,11 +507,11 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
 #pragma unroll
         for (int q = 0; q < P * FT; ++q) {
             const int h = q / FT, j = q % FT;
-            if (q < P * HN) wa[q / HN][q % HN] = read((part<E4M3, BN, BT, MT, KG, NEXT, 1>() + (WIDE ? 0 : grp) * (BN * 4)), at_w + q % HN * (MT * RC), q / HN);
+            if (q < P * HN) wa[q / HN][q % HN] = read(stage_w(Const<NEXT>{}, Const<1>{}), at_w + q % HN * (MT * RC), q / HN);
             fetch_xa(st, q * XA / (P * FT), (q + 1) * XA / (P * FT), k + B);
 #pragma unroll
             for (int i = 0; i < HN; ++i) acc[1][j][i] = S::mma(wb[h][i], x[h][j], acc[1][j][i]);
-            x[h][j] = read((part<E4M3, BN, BT, MT, KG, NEXT, 0>() + (WIDE ? 0 : grp) * (BT * 8)), at_x + j * (MT * RC), h);
+            x[h][j] = read(stage_x(Const<NEXT>{}), at_x + j * (MT * RC), h);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -600,7 +613,8 @@ __device__ inline void linear_tile(const LinearArgs &a, int tiles_n, int tiles_t
     // time, so that a lane finishes 8 neighbouring outputs of a token.
     constexpr int PT = 32 / MT;                                  // token tiles at a time
     static_assert(32 * CW * 2 <= BT * 8, "two wavefronts' sums fit one token part");
-    i32x4 *mine = ((wave & 2) ? (part<E4M3, BN, BT, MT, KG, 1, 0>() + grp * (BT * 8)) : (part<E4M3, BN, BT, MT, KG, 0, 0>() + grp * (BT * 8))) + (wave & 1) * (32 * CW);
+    i32x4 *const sums = (wave & 2) ? part<E4M3, BN, BT, MT, KG, 1, 0>() : part<E4M3, BN, BT, MT, KG, 0, 0>();
+    i32x4 *const mine = sums + grp * (BT * 8) + (wave & 1) * (32 * CW);
     const int lane_n = lane % LPT;
 #pragma unroll 1
     for (int p = 0; p < FT / PT; ++p) {

@@ -547,7 +547,8 @@ __global__ __launch_bounds__(kPlaceWaves * 64) void route_place_kernel(RouteArgs
     // this block's pairs, each wavefront a contiguous range
     const int b0 = g0 * kTileT * a.k, b1 = min(n, b0 + tiles * kTileT * a.k);
     const int len = b1 - b0;
-    const int p0 = b0 + (int)((long long)len * wave / kPlaceWaves), p1 = b0 + (int)((long long)len * (wave + 1) / kPlaceWaves);
+    const int p0 = b0 + (int)((long long)len * wave / kPlaceWaves);
+    const int p1 = b0 + (int)((long long)len * (wave + 1) / kPlaceWaves);
     s_tot[wave][lane] = tot;
     s_pre[wave][lane] = pre;
     s_cnt[wave][lane] = 0;
