@@ -134,3 +134,29 @@ def test_host_tensors_are_refused():
         B.moe_linear(h, F, 4, 64, 256, B.MOE_LINEAR_FP16, F, ws=F, ws_bytes=1 << 30, stream=0)
     with pytest.raises(ValueError, match="one GPU"):
         B.moe_route_scored(F, h, None, 4, 256, 8, 2, B.route_rule(), None, F, F, F, F, F, F, F, F, 1 << 20, stream=0)
+
+
+def test_layers_refuse_weights_of_other_shapes():
+    torch = pytest.importorskip("torch")
+    from w4a16_routed_expert_amd.layer import DecodeStack, DenseFFN, RoutedExpertLayer
+    up, down = torch.zeros(96, 64, dtype=torch.float16), torch.zeros(64, 96, dtype=torch.float16)
+    f8 = up.to(torch.float8_e4m3fn)
+    f32 = torch.zeros(96)
+    for args, kw in (((up.float(), down), {}), ((up, down.float()), {}), ((up, down.t()[:, :32]), {}),
+                     ((up, down), dict(up_scale=f32)), ((f8, down), {}), ((f8, down), dict(up_scale=f32[:95])),
+                     ((f8, down), dict(up_scale=f32.half())),
+                     ((up, down), dict(up_bias=f32[:64])), ((up, down), dict(down_bias=f32)),
+                     ((up, down), dict(up_bias=torch.zeros(192)[::2]))):
+        with pytest.raises(ValueError):
+            DenseFFN(*args, **kw)
+    rule = B.route_rule(score=B.MOE_SCORE_SIGMOID)
+    for kw in (dict(rule=rule, bias=f32), dict(select_bias=f32), dict(rule=rule, select_bias=f32[:7]),
+               dict(rule=rule, select_bias=torch.zeros(8).double())):
+        with pytest.raises(ValueError):
+            RoutedExpertLayer(256, 256, 8, 2, torch.zeros(1, 1, dtype=torch.uint8), up, **kw)
+
+    class Layer:
+        H, device = 64, "cpu"
+    for norms in ([f32[:64].half()], [f32[:64].half(), f32.half()], [f32[:64].half(), f32[:64]]):
+        with pytest.raises(ValueError):
+            DecodeStack([Layer(), Layer()], [None, None], norms=norms)

@@ -34,6 +34,7 @@ class RoutedExpertLayer:
             raise ValueError("routing by scores takes no logit bias (select_bias biases the choice)")
         if rule is None and select_bias is not None:
             raise ValueError("select_bias goes with a routing rule")
+        _vector("select_bias", select_bias, E, torch.float32)
         self.H, self.I, self.E, self.k = H, I, E, k
         self.rule, self.select_bias = rule, select_bias
         self.row_bytes, self.offsets6 = B.moe_expert_row_bytes(H, I)
@@ -272,6 +273,12 @@ class RoutedExpertLayer:
                              if st == B.MOE_ERR_ABSENT_EXPERT else "expert FFN status word set")
 
 
+def _vector(name: str, t, n: int, dtype):
+    """Refuses a vector (None passes) that is not n contiguous values of dtype."""
+    if t is not None and (tuple(t.shape) != (n,) or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{name} must be {n} contiguous values of {dtype}")
+
+
 @contextlib.contextmanager
 def _ordered(stream):
     """New buffers for work on `stream`: what the current stream does with their memory comes after the
@@ -440,6 +447,9 @@ class DenseFFN:
             raise ValueError("w_up must be float16 or float8_e4m3fn, w_down float16")
         if tuple(w_down.shape) != (self.H, self.I) or self.e4m3 != (up_scale is not None):
             raise ValueError("w_down must be [H, I], and up_scale goes with e4m3 weights")
+        _vector("up_scale", up_scale, self.I, torch.float32)
+        _vector("up_bias", up_bias, self.I, torch.float32)
+        _vector("down_bias", down_bias, self.H, torch.float32)
         self.w_up, self.w_down, self.up_scale = w_up, w_down, up_scale
         self.up_bias, self.down_bias, self.act = up_bias, down_bias, act
         self.device = torch.device(device)
@@ -457,6 +467,12 @@ class DenseFFN:
             out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """x: float16 [T, H], or the 8-bit activations with x_scale (float32 [T])."""
         T = x.shape[0]
+        if tuple(x.shape) != (T, self.H) or x.dtype != self.w_up.dtype:
+            raise ValueError(f"x must be [T, {self.H}] of {self.w_up.dtype}")
+        _vector("x_scale", x_scale, T, torch.float32)
+        for name, t in (("residual", residual), ("out", out)):
+            if t is not None and (tuple(t.shape) != (T, self.H) or t.dtype != torch.float16):
+                raise ValueError(f"{name} must be float16 [{T}, {self.H}]")
         if T > self.max_T:
             with _ordered(stream):
                 self._alloc(T)
@@ -502,6 +518,8 @@ class DecodeStack:
         self.norms, self.eps = None if norms is None else list(norms), eps
         if self.norms is not None and len(self.norms) != self.L:
             raise ValueError("one norm weight per layer")
+        for l, n in enumerate(self.norms or []):
+            _vector(f"norms[{l}]", n, self.layers[l].H, torch.float16)
         if self.norms is None and any(isinstance(l, DenseFFN) and l.e4m3 for l in self.layers):
             raise ValueError("a dense layer with e4m3 weights needs norms (they make its 8-bit activations)")
         lay = self.layers[0]
